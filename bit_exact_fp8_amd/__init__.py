@@ -6,3 +6,5 @@ not load the library; the first call does, and fails loudly if it is missing.
 """
 from .api import (EmuError, accumulate, abi_version, library_path, scaled_mm,  # noqa: F401
                   workspace_bytes)
+from .operators import (TokenLogprobs, add_rms_norm_backward, add_rms_norm_quant, int8_scaled_mm,  # noqa: F401
+                        token_logprobs, token_logprobs_backward)

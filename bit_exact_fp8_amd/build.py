@@ -4,8 +4,9 @@ The main kernel's variants (block width x format pair) are separate
 translation units of emu_variant.hip (and of emu_cin_variant.hip for the
 chains from incoming accumulators), compiled in parallel and linked with the
 dispatcher, the combine kernel, the deferred-infinity kernels
-(emu_specials.hip), the no-allocation entry point (emu_noalloc.hip) and the
-C ABI."""
+(emu_specials.hip), the no-allocation entry point (emu_noalloc.hip), the C
+ABI and the operators beside the product (emu_norm.hip, emu_int8.hip,
+emu_logprobs.hip, ops_api.cpp)."""
 from __future__ import annotations
 
 import os
@@ -38,6 +39,8 @@ def _units(objdir: str):
              (os.path.join(CSRC, "emu_specials.hip"), os.path.join(objdir, "emu_specials.o"), []),
              (os.path.join(CSRC, "emu_noalloc.hip"), os.path.join(objdir, "emu_noalloc.o"), []),
              (os.path.join(CSRC, "emu_api.cpp"), os.path.join(objdir, "emu_api.o"), [])]
+    for name in ("emu_norm.hip", "emu_int8.hip", "emu_logprobs.hip", "ops_api.cpp"):
+        units.append((os.path.join(CSRC, name), os.path.join(objdir, name.split(".")[0] + ".o"), []))
     for b, xf, wf in VARIANTS:
         defs = [f"-DEMU_VARIANT_BLK={b}", f"-DEMU_VARIANT_XF={xf}", f"-DEMU_VARIANT_WF={wf}"]
         units.append((os.path.join(CSRC, "emu_variant.hip"), os.path.join(objdir, f"emu_variant_{b}_{xf}{wf}.o"), defs))

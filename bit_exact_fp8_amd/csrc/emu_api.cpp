@@ -10,6 +10,7 @@
 #include "../../include/emu_fp8gemm.h"
 #include "emu_internal.h"
 #include "fp_round.h"
+#include "ops_internal.h"
 
 namespace {
 
@@ -463,6 +464,20 @@ emu_status scaled_mm_in_scratch(const uint8_t *x, emu_fp8_format x_fmt, int64_t 
     return scaled_mm_call(x, x_fmt, ldx, w, w_fmt, ldw, M, N, K, scale_x, scale_w, scale_result, out,
                           (int)out_dtype < 0 ? 1000 : (int)out_dtype, ldo, fast_accum, split_S, profile, ws,
                           ws_bytes, stream, plan, (int64_t)scratch_bytes);
+}
+
+}  // namespace emu
+
+namespace emu {
+
+emu_status set_error(emu_status s, const char *text) noexcept
+{
+    try {
+        g_last_error = text;
+    } catch (...) {
+        g_last_error.clear();
+    }
+    return s;
 }
 
 }  // namespace emu
