@@ -40,7 +40,10 @@ def _units(objdir: str):
              (os.path.join(CSRC, "emu_noalloc.hip"), os.path.join(objdir, "emu_noalloc.o"), []),
              (os.path.join(CSRC, "emu_api.cpp"), os.path.join(objdir, "emu_api.o"), [])]
     for name in ("emu_norm.hip", "emu_int8.hip", "emu_logprobs.hip", "ops_api.cpp"):
-        units.append((os.path.join(CSRC, name), os.path.join(objdir, name.split(".")[0] + ".o"), []))
+        # the accumulators of the int8 tiles stay in ordinary registers: the
+        # compiler otherwise copies them to and fro in the loop
+        extra = ["-mllvm", "-amdgpu-mfma-vgpr-form=true"] if name == "emu_int8.hip" else []
+        units.append((os.path.join(CSRC, name), os.path.join(objdir, name.split(".")[0] + ".o"), extra))
     for b, xf, wf in VARIANTS:
         defs = [f"-DEMU_VARIANT_BLK={b}", f"-DEMU_VARIANT_XF={xf}", f"-DEMU_VARIANT_WF={wf}"]
         units.append((os.path.join(CSRC, "emu_variant.hip"), os.path.join(objdir, f"emu_variant_{b}_{xf}{wf}.o"), defs))

@@ -158,7 +158,9 @@ emu_status emu_int8_scaled_mm(const int8_t *a, int64_t lda, const int8_t *w, int
     if (!aligned_to(out, size_of(out_dtype)) || !aligned_to(scale_a, 4) || !aligned_to(scale_w, 4) ||
         (bias && !aligned_to(bias, size_of(bias_dtype))))
         return invalid("a pointer is not aligned to its element");
-    const bool aligned = aligned_to(a, 16) && aligned_to(w, 16) && lda % 16 == 0 && ldw % 16 == 0;
+    // (a tile's offsets from its first row have to stay within 31 bits)
+    const bool aligned = aligned_to(a, 16) && aligned_to(w, 16) && lda % 16 == 0 && ldw % 16 == 0 &&
+                         lda <= EMU_INT8_MAX_ALIGNED_LD && ldw <= EMU_INT8_MAX_ALIGNED_LD;
     const int64_t need = emu::int8_mm_workspace(M, N, K, aligned);
     if ((int64_t)workspace_bytes < need || (need > 0 && !workspace))
         return set_error(EMU_ERR_WORKSPACE, "workspace smaller than emu_int8_scaled_mm_workspace");

@@ -27,7 +27,8 @@ DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.float8_e4m
          torch.int8: 5}
 QUANT_DTYPES = (torch.float8_e4m3fn, torch.float8_e5m2, torch.int8)
 FLOAT_DTYPES = (torch.bfloat16, torch.float16, torch.float32)
-MAX_TOP_TOKENS = 64   # EMU_MAX_TOP_TOKENS
+MAX_TOP_TOKENS = 64          # EMU_MAX_TOP_TOKENS
+INT8_MAX_ALIGNED_LD = 1 << 22   # EMU_INT8_MAX_ALIGNED_LD
 
 _LIB = None
 
@@ -251,7 +252,8 @@ def int8_scaled_mm(mat1: torch.Tensor, mat2: torch.Tensor, scale_a: torch.Tensor
         ldo = out.stride(0) if M > 1 else N
     lib = _lib()
     ap, wp = a.data_ptr(), w.data_ptr()
-    nbytes = lib.emu_int8_scaled_mm_workspace(M, N, K, not (ap | wp | lda | ldw) & 15)
+    aligned = not (ap | wp | lda | ldw) & 15 and lda <= INT8_MAX_ALIGNED_LD and ldw <= INT8_MAX_ALIGNED_LD
+    nbytes = lib.emu_int8_scaled_mm_workspace(M, N, K, aligned)
     ws = _workspace(nbytes, dev)
     _launch(dev, lib.emu_int8_scaled_mm, ap, lda, wp, ldw, M, N, K, scale_a.data_ptr(), per_a, scale_b.data_ptr(),
             per_b, _ptr(bias), bdt, out.data_ptr(), DTYPE[out_dtype], ldo, _ptr(ws), nbytes)

@@ -96,8 +96,9 @@ EMU_API size_t emu_add_rms_norm_backward_workspace(int64_t T, int64_t n);
  * workspace: emu_int8_scaled_mm_workspace(...) bytes, 16-byte aligned; NULL
  * where that is 0.  It depends on the pointers' alignment and the leading
  * dimensions besides the sizes: `aligned` says that a, w, lda and ldw are all
- * multiples of 16.
+ * multiples of 16 and the last two at most EMU_INT8_MAX_ALIGNED_LD.
  */
+#define EMU_INT8_MAX_ALIGNED_LD (INT64_C(1) << 22)
 EMU_API emu_status emu_int8_scaled_mm(const int8_t *a, int64_t lda, const int8_t *w, int64_t ldw,
                                       int64_t M, int64_t N, int64_t K,
                                       const float *scale_a, int a_per_row, const float *scale_w, int w_per_row,

@@ -768,3 +768,30 @@ def test_binding_refusals(dev):
         fw.token_logprobs(x.clone().requires_grad_(), tok)
     with torch.no_grad():
         fw.token_logprobs(x.clone().requires_grad_(), tok)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", [(260, 260, 16), (513, 390, 1360), (1024, 8192, 384), (2048, 2048, 272), (3000, 3000, 512),
+                                   (100, 100, 16384), (129, 70, 8208), (2100, 2300, 1000), (2300, 2100, 1111)])
+def test_int8_mm_tiles(dev, M, N, K):
+    """Every tile, whole and ragged, a split of K, stages that end within K."""
+    check_mm(dev, M, N, K, BF, SF, seed=3)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", [(2 ** 18 + 5, 33, 16), (2 ** 18 + 70, 20, 33), (3, 2 ** 20 + 3, 16), (70, 2 ** 20 + 65, 16)])
+def test_int8_mm_slices(dev, M, N, K):
+    """More rows or columns than one launch takes."""
+    check_mm(dev, M, N, K, HF, HF, seed=4)
+
+
+@pytest.mark.gpu
+def test_int8_mm_wide_rows(dev):
+    """Leading dimensions beyond the tiles' 31-bit offsets: rows laid out anew."""
+    big = torch.zeros(300, 1 << 23, dtype=I8, device=dev)
+    gen = rng(5)
+    a, w = int8(gen, 300, 512), int8(gen, 200, 512)
+    big[:, 64:576] = a.to(dev)
+    sa = torch.full((1,), 0.01, device=dev)
+    y = fw.int8_scaled_mm(big[:, 64:576], w.to(dev).t(), sa, sa, out_dtype=SF)
+    assert torch.equal(y.cpu(), mm_want(a, w, sa.cpu(), sa.cpu(), None, SF))
