@@ -21,6 +21,16 @@ namespace emu {
 
 namespace {
 
+template <typename Z>
+__device__ __forceinline__ f32x8 load8_fill(const Z *p, int64_t c, int64_t end, float fill)
+{
+    if (c + 8 <= end) return widen<Z>(load8(p + c));
+    f32x8 r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = c + i < end ? (float)p[c + i] : fill;
+    return r;
+}
+
 constexpr int kThreads = 256;
 constexpr int kTile = kThreads * 8;          // logits that a workgroup reads at once
 constexpr float kLowest = -3.402823466e+38f;
@@ -163,7 +173,7 @@ __device__ void top_of_segment(const Z *z, int64_t s0, int64_t s1, int k, uint64
         for (int j = t; j < winners * iters; j += kThreads) {
             const int64_t c = s0 + (int64_t)(j / winners) * kTile + (int)sh.winner[j % winners] * 8;
             if (c >= s1) continue;
-            const f32x8 v = load8_row(z, c, s1, -INFINITY);
+            const f32x8 v = load8_fill(z, c, s1, -INFINITY);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 if (v[e] >= least && c + e < s1) {
@@ -253,8 +263,8 @@ __global__ __launch_bounds__(kThreads) void logp_rows(LogpParams p, int64_t firs
         a.u += u[0] + u[1];
     };
     int64_t c = c0;
-    for (; c + kTile + 8 <= s1; c += 2 * kTile) take(load8(z + c), load8(z + c + kTile), c);
-    if (c < s1) take(load8_row(z, c, s1, -INFINITY), load8_row(z, c + kTile, s1, -INFINITY), c);
+    for (; c + kTile + 8 <= s1; c += 2 * kTile) take(widen<Z>(load8(z + c)), widen<Z>(load8(z + c + kTile)), c);
+    if (c < s1) take(load8_fill(z, c, s1, -INFINITY), load8_fill(z, c + kTile, s1, -INFINITY), c);
 
     uint64_t mine = 0;
     if (TOP && c0 < s1) {
@@ -410,11 +420,11 @@ __global__ __launch_bounds__(kThreads) void logp_grad_rows(LogpGradParams p, int
     };
     if (H) __syncthreads();
     for (int64_t c = s0 + threadIdx.x * 8; c < s1; c += kTile) {
-        const f32x8 x = load8_row(z, c, s1);
+        const f32x8 x = load8_fill(z, c, s1, 0.0f);
         f32x8 r;
 #pragma unroll
         for (int j = 0; j < 8; ++j) r[j] = empty ? 0.0f : value(x[j]);
-        store8_row(grad, c, s1, r);
+        store8_row(grad + s0, (int)(c - s0), (int)(s1 - s0), r);
     }
     if (!H || empty) return;
     __syncthreads();

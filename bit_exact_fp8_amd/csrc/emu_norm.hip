@@ -3,8 +3,11 @@
 // Forward: v = x + residual, y = v r w with r = 1 / sqrt(mean(v^2) + eps),
 // codes of y / scale.  Each value is needed three times (for the mean, for
 // the row's largest |y|, for its code), so a row is held in registers and
-// read once.
+// read once.  16384 x 8192 bf16: 162 us with a given scale, 5.8 TB/s; with
+// each row's own, which adds a reduction and a pass over the registers, 180.
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 #include "ops_device.h"
 #include "ops_internal.h"
@@ -13,33 +16,65 @@ namespace emu {
 
 namespace {
 
-// 8 codes of y / scale, cut to +-Q and rounded to nearest even.  The division
-// is IEEE's, not a product with the reciprocal: codes are those of the
-// definition also next to a tie, and at some 10 instructions a value it hides
-// behind the row's loads.  The comparisons keep a NaN (fmin / fmax drop it).
+// A row's way from v to codes: u = v 2^e w with 2^e near r (the power of two
+// changes no digit and keeps v w from overflowing), then u f with
+// f = r 2^-e / scale, made in 64 bits and kept as the sum of two binary32
+// values.  A code is so off by two roundings, not by the five of v r, times
+// w, over scale with an r of 32 bits: next to a border fewer codes fall to
+// the other side, and no division is left.  A scale under 2^-100, whose f may
+// overflow, divides.
+struct Factor {
+    float power, hi, lo;  // 2^e; f
+    float rest, scale;    // r 2^-e
+};
+__device__ __forceinline__ Factor factor_of(double r)
+{
+    Factor f;
+    const int e = r > 0.0 && r < 1e300 ? __builtin_amdgcn_frexp_exp(r) : 0;
+    f.power = __builtin_amdgcn_ldexpf(1.0f, e);
+    f.rest = (float)(r / (double)f.power);
+    f.hi = f.lo = f.scale = 0.0f;
+    return f;
+}
+__device__ __forceinline__ void set_scale(Factor &f, double r, float scale)
+{
+    const double q = r / (double)f.power / (double)scale;
+    f.hi = (float)q;
+    f.lo = (float)(q - (double)f.hi);
+    f.scale = scale;
+}
+
+// Cut to +-Q; the comparisons keep a NaN (fmin / fmax drop it).
 template <int Q>
-__device__ __forceinline__ float cut(float v, float scale)
+__device__ __forceinline__ float cut(float v)
 {
     constexpr float most = Q == EMU_DT_INT8 ? 127.0f : Q == EMU_DT_E4M3FN ? 448.0f : 57344.0f;
-    v = v / scale;
     return v > most ? most : v < -most ? -most : v;
 }
 
+// 8 codes, rounded to nearest even.
 template <int Q>
-__device__ __forceinline__ uint2 codes8(const f32x8 &y, float scale)
+__device__ __forceinline__ uint2 codes8(const f32x8 &u, const Factor &f)
 {
+    f32x8 y;
+    if (f.scale >= 7.888609052e-31f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = __builtin_fmaf(u[i], f.hi, u[i] * f.lo);
+    } else {
+        y = u * f.rest / f.scale;
+    }
     uint32_t r[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         float c[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) c[i] = cut<Q>(y[4 * j + i], scale);
+        for (int i = 0; i < 4; ++i) c[i] = cut<Q>(y[4 * j + i]);
         if (Q == EMU_DT_INT8) {
             uint32_t b = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float f = c[i] == c[i] ? c[i] : 0.0f;
-                b |= ((uint32_t)(int)rintf(f) & 0xFFu) << (8 * i);
+                const float k = c[i] == c[i] ? c[i] : 0.0f;
+                b |= ((uint32_t)(int)rintf(k) & 0xFFu) << (8 * i);
             }
             r[j] = b;
         } else if (Q == EMU_DT_E4M3FN) {
@@ -53,26 +88,38 @@ __device__ __forceinline__ uint2 codes8(const f32x8 &y, float scale)
     return make_uint2(r[0], r[1]);
 }
 
-struct uint2_u {
-    uint32_t x, y;
+template <typename T>
+struct Bytes {
+    T v;
 } __attribute__((packed, aligned(1)));
 
-__device__ __forceinline__ void store_codes(uint8_t *row, int64_t c, int64_t n, const uint2 &r)
+__device__ __forceinline__ void store_codes(uint8_t *row, int c, int n, const uint2 &r)
 {
+    uint64_t v = (uint64_t)r.y << 32 | r.x;
+    uint8_t *p = row + c;
     if (c + 8 <= n) {
-        *reinterpret_cast<uint2_u *>(row + c) = uint2_u{r.x, r.y};
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (c + i < n) row[c + i] = (uint8_t)((i < 4 ? r.x : r.y) >> (8 * (i & 3)));
+        reinterpret_cast<Bytes<uint64_t> *>(p)->v = v;
+        return;
     }
+    const int left = c < n ? n - c : 0;
+    if (left & 4) {
+        reinterpret_cast<Bytes<uint32_t> *>(p)->v = (uint32_t)v;
+        p += 4;
+        v >>= 32;
+    }
+    if (left & 2) {
+        reinterpret_cast<Bytes<uint16_t> *>(p)->v = (uint16_t)v;
+        p += 2;
+        v >>= 16;
+    }
+    if (left & 1) *p = (uint8_t)v;
 }
 
-__device__ __forceinline__ uint2 codes8_any(int q_dtype, const f32x8 &y, float scale)
+__device__ __forceinline__ uint2 codes8_any(int q_dtype, const f32x8 &u, const Factor &f)
 {
-    if (q_dtype == EMU_DT_INT8) return codes8<EMU_DT_INT8>(y, scale);
-    if (q_dtype == EMU_DT_E4M3FN) return codes8<EMU_DT_E4M3FN>(y, scale);
-    return codes8<EMU_DT_E5M2>(y, scale);
+    if (q_dtype == EMU_DT_INT8) return codes8<EMU_DT_INT8>(u, f);
+    if (q_dtype == EMU_DT_E4M3FN) return codes8<EMU_DT_E4M3FN>(u, f);
+    return codes8<EMU_DT_E5M2>(u, f);
 }
 
 __device__ __forceinline__ float most_of(int q_dtype)
@@ -82,6 +129,10 @@ __device__ __forceinline__ float most_of(int q_dtype)
 
 // Smallest own scale: a row of zeros divides by it and gives zeros.
 constexpr float kLeastScale = 1.17549435e-38f;  // 2^-126
+__device__ __forceinline__ float own_scale(float most, const Factor &f, int q_dtype)
+{
+    return __builtin_elementwise_maximum(most * f.rest / most_of(q_dtype), kLeastScale);
+}
 
 // W waves hold one row, VPT vectors of 8 values in each lane: n <= W * VPT * 512.
 // R: no residual, or its element type.
@@ -90,33 +141,41 @@ template <typename X, typename R, int W, int VPT>
 __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_rows(NormParams p)
 {
     constexpr bool kRes = !__is_same(R, NoRes);
-    __shared__ float lds[2][W];
+    __shared__ double sums[W];
+    __shared__ float maxima[W];
     const int lane = threadIdx.x & 63;
-    const int wave = W == 1 ? 0 : threadIdx.x >> 6;
-    const int64_t row = W == 1 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+    const int wave = W == 1 ? 0 : wave_index();
+    const int64_t row = W == 1 ? (int64_t)blockIdx.x * 4 + wave_index() : blockIdx.x;
     if (W == 1 && row >= p.T) return;
-    const int64_t n = p.n;
+    const int n = (int)p.n;
+    __builtin_assume(n >= 8);
     const X *x = static_cast<const X *>(p.x) + row * p.ldx;
-    const int64_t c0 = (int64_t)(wave * 64 + lane) * 8;
+    const int c0 = (wave * 64 + lane) * 8;
 
-    f32x8 v[VPT], w[VPT];
+    f32x8 v[VPT];
+    {
+        Raw8<X> xr[VPT];
+        Raw8<std::conditional_t<kRes, R, X>> rr[VPT];
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) v[i] = load8_row(x, c0 + i * (W * 512), n);
-    if constexpr (kRes) {
-        const R *res = static_cast<const R *>(p.res) + row * p.ldres;
+        for (int i = 0; i < VPT; ++i) {
+            const int c = c0 + i * (W * 512);
+            xr[i] = fetch8(x, c, n);
+            if constexpr (kRes) rr[i] = fetch8(static_cast<const R *>(p.res) + row * p.ldres, c, n);
+        }
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) v[i] += load8_row(res, c0 + i * (W * 512), n);
+        for (int i = 0; i < VPT; ++i) {
+            const int c = c0 + i * (W * 512);
+            v[i] = settle8<X>(xr[i], c, n);
+            if constexpr (kRes) v[i] += settle8<R>(rr[i], c, n);
+        }
     }
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) w[i] = load8_any(p.weight, p.w_dtype, c0 + i * (W * 512), n);
 
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) s += v[i][j] * v[i][j];
-    s = row_sum<W>(s, lds[0], wave, lane);
-    const float r = 1.0f / sqrtf(s / (float)n + p.eps);
+    const double r = 1.0 / sqrt(row_sum<W>((double)s, sums, wave, lane) / (double)n + (double)p.eps);
 
     if constexpr (kRes) {
         if (p.h) {
@@ -125,9 +184,12 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_rows(NormParams p)
             for (int i = 0; i < VPT; ++i) store8_row(h, c0 + i * (W * 512), n, v[i]);
         }
     }
+    Factor f = factor_of(r);
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) v[i] = v[i] * r * w[i];
-
+    for (int i = 0; i < VPT; ++i) {
+        const int c = c0 + i * (W * 512);
+        v[i] = v[i] * f.power * settle8_any(fetch8_any(p.weight, p.w_dtype, c, n), p.w_dtype, c, n);
+    }
     float scale;
     if (p.scale) {
         scale = *p.scale;
@@ -137,87 +199,99 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_rows(NormParams p)
         for (int i = 0; i < VPT; ++i)
 #pragma unroll
             for (int j = 0; j < 8; ++j) a = __builtin_elementwise_maximum(a, __builtin_fabsf(v[i][j]));
-        a = row_max<W>(a, lds[1], wave, lane);
-        scale = __builtin_elementwise_maximum(a / most_of(p.q_dtype), kLeastScale);
+        scale = own_scale(row_max<W>(a, maxima, wave, lane), f, p.q_dtype);
         if (wave == 0 && lane == 0) p.row_scales[row] = scale;
     }
+    set_scale(f, r, scale);
     uint8_t *q = static_cast<uint8_t *>(p.q) + row * p.ldq;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int64_t c = c0 + i * (W * 512);
-        if (c < n) store_codes(q, c, n, codes8_any(p.q_dtype, v[i], scale));
+        const int c = c0 + i * (W * 512);
+        if (c < n) store_codes(q, c, n, codes8_any(p.q_dtype, v[i], f));
     }
 }
 
-// Rows too long for registers: three passes over the row, by one workgroup.
+// Rows too long for registers (or of fewer than 8 values): three passes over
+// the row, by one workgroup.
 // h is stored in the last one, after its element's last load, since it may be
 // the residual.
 template <typename X, typename R>
 __global__ __launch_bounds__(1024) void norm_long_rows(NormParams p)
 {
     constexpr bool kRes = !__is_same(R, NoRes);
-    __shared__ float lds[2][16];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t row = blockIdx.x, n = p.n;
+    __shared__ double sums[16];
+    __shared__ float maxima[16];
+    const int lane = threadIdx.x & 63, wave = wave_index();
+    const int64_t row = blockIdx.x;
+    const int n = (int)p.n;
     const X *x = static_cast<const X *>(p.x) + row * p.ldx;
-    const auto value = [&](int64_t c) {
-        f32x8 v = load8_row(x, c, n);
-        if constexpr (kRes) v += load8_row(static_cast<const R *>(p.res) + row * p.ldres, c, n);
-        return v;
+    const auto weight = [&](int c) { return settle8_any(fetch8_any(p.weight, p.w_dtype, c, n), p.w_dtype, c, n); };
+    const auto value = [&](int c) {
+        const Raw8<X> xr = fetch8(x, c, n);
+        if constexpr (kRes) {
+            const Raw8<R> rr = fetch8(static_cast<const R *>(p.res) + row * p.ldres, c, n);
+            return settle8<X>(xr, c, n) + settle8<R>(rr, c, n);
+        } else {
+            return settle8<X>(xr, c, n);
+        }
     };
-    float s = 0.0f;
-    for (int64_t c = threadIdx.x * 8; c < n; c += 8192) {
+    double s = 0.0;
+    for (int c = threadIdx.x * 8; c < n; c += 8192) {
         const f32x8 v = value(c);
         float t = 0.0f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) t += v[j] * v[j];
-        s += t;
+        s += (double)t;
     }
-    s = row_sum<16>(s, lds[0], wave, lane);
-    const float r = 1.0f / sqrtf(s / (float)n + p.eps);
+    const double r = 1.0 / sqrt(row_sum<16>(s, sums, wave, lane) / (double)n + (double)p.eps);
+    Factor f = factor_of(r);
     float scale;
     if (p.scale) {
         scale = *p.scale;
     } else {
         float a = 0.0f;
-        for (int64_t c = threadIdx.x * 8; c < n; c += 8192) {
-            const f32x8 y = value(c) * r * load8_any(p.weight, p.w_dtype, c, n);
+        for (int c = threadIdx.x * 8; c < n; c += 8192) {
+            const f32x8 u = value(c) * f.power * weight(c);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) a = __builtin_elementwise_maximum(a, __builtin_fabsf(y[j]));
+            for (int j = 0; j < 8; ++j) a = __builtin_elementwise_maximum(a, __builtin_fabsf(u[j]));
         }
-        a = row_max<16>(a, lds[1], wave, lane);
-        scale = __builtin_elementwise_maximum(a / most_of(p.q_dtype), kLeastScale);
+        scale = own_scale(row_max<16>(a, maxima, wave, lane), f, p.q_dtype);
         if (threadIdx.x == 0) p.row_scales[row] = scale;
     }
+    set_scale(f, r, scale);
     uint8_t *q = static_cast<uint8_t *>(p.q) + row * p.ldq;
-    for (int64_t c = threadIdx.x * 8; c < n; c += 8192) {
+    for (int c = threadIdx.x * 8; c < n; c += 8192) {
         const f32x8 v = value(c);
         if constexpr (kRes) {
             if (p.h) store8_row(static_cast<R *>(p.h) + row * p.ldh, c, n, v);
         }
-        store_codes(q, c, n, codes8_any(p.q_dtype, v * r * load8_any(p.weight, p.w_dtype, c, n), scale));
+        store_codes(q, c, n, codes8_any(p.q_dtype, v * f.power * weight(c), f));
     }
 }
 
+// Few waves with more values each need fewer barriers, many with few have
+// more rows in flight: 16384 x 2048 takes 44 us on 2 waves of 16 values a
+// lane, 62 on 4 of 8; 4096 x 16384 98 us on 8 of 32, 117 on 16 of 16; 16384 x
+// 4096 84 us on 4 of 16, 92 on 2 of 32.
 template <typename X, typename R>
 hipError_t launch_norm_of(const NormParams &p, hipStream_t stream)
 {
     const int64_t n = p.n, T = p.T;
     const dim3 rows((unsigned)T), rows4((unsigned)((T + 3) / 4));
-    if (n <= 512)
+    if (n < 8 || n > 16384)
+        hipLaunchKernelGGL((norm_long_rows<X, R>), rows, dim3(1024), 0, stream, p);
+    else if (n <= 512)
         hipLaunchKernelGGL((norm_rows<X, R, 1, 1>), rows4, dim3(256), 0, stream, p);
     else if (n <= 1024)
         hipLaunchKernelGGL((norm_rows<X, R, 1, 2>), rows4, dim3(256), 0, stream, p);
     else if (n <= 2048)
-        hipLaunchKernelGGL((norm_rows<X, R, 4, 1>), rows, dim3(256), 0, stream, p);
+        hipLaunchKernelGGL((norm_rows<X, R, 2, 2>), rows, dim3(128), 0, stream, p);
     else if (n <= 4096)
         hipLaunchKernelGGL((norm_rows<X, R, 4, 2>), rows, dim3(256), 0, stream, p);
     else if (n <= 8192)
         hipLaunchKernelGGL((norm_rows<X, R, 8, 2>), rows, dim3(512), 0, stream, p);
-    else if (n <= 16384)
-        hipLaunchKernelGGL((norm_rows<X, R, 16, 2>), rows, dim3(1024), 0, stream, p);
     else
-        hipLaunchKernelGGL((norm_long_rows<X, R>), rows, dim3(1024), 0, stream, p);
+        hipLaunchKernelGGL((norm_rows<X, R, 8, 4>), rows, dim3(512), 0, stream, p);
     return hipGetLastError();
 }
 
@@ -235,57 +309,56 @@ hipError_t launch_norm_x(int res_dtype, const NormParams &p, hipStream_t stream)
 // grad_weight adds g n over all rows.  A workgroup takes rows blockIdx,
 // blockIdx + parts, ... of the grid, holds a row in registers while its two
 // sums are made (together, one barrier), and adds its rows' g n in binary32
-// registers; it stores them once, and grad_weight_kernel adds the parts.  The
-// next row's loads are issued before this row's sums are waited for.
+// registers; it stores them once, and grad_weight_kernel adds the parts.
+// Enough workgroups share a CU for one's loads to cover the other's sums: to
+// read the next row ahead as well gains nothing.  8192 x 8192 bf16 with
+// grad_h: 106 + 5 us, 4.9 TB/s, the rate of a large copy.
 
-template <typename E>
-__device__ __forceinline__ f32x8 widen(const E &v)
-{
-    return __builtin_convertvector(v, f32x8);
-}
-
-template <typename G, typename H, int W, int VPT>
-__global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_grad_rows(NormGradParams p, int64_t parts)
+// D: grad_h's type.
+template <typename G, typename H, typename D, int W, int VPT>
+__global__ __launch_bounds__(W == 1 ? 256 : W * 64, 4) void norm_grad_rows(NormGradParams p, int64_t parts)
 {
     constexpr int kRows = W == 1 ? 4 : 1;  // rows at a time in a workgroup
     __shared__ float2 lds[2][W];
     __shared__ float share[W == 1 ? 3 * VPT * 512 : 1];
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wv = wave_index();
     const int wave = W == 1 ? 0 : wv;
-    const int64_t n = p.n, step = parts * kRows;
-    const int64_t c0 = (int64_t)(wave * 64 + lane) * 8;
-    const G *g = static_cast<const G *>(p.g);
-    const H *h = static_cast<const H *>(p.h);
+    const int n = (int)p.n;
+    const int64_t step = parts * kRows;
+    __builtin_assume(n >= 8);
+    const int c0 = (wave * 64 + lane) * 8;
 
     f32x8 gw[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) gw[i] = 0.0f;
-    typename Vec8<G>::type gn[VPT];
-    typename Vec8<H>::type hn[VPT];
+    const auto weight = [&](int c) { return settle8_any(fetch8_any(p.weight, p.w_dtype, c, n), p.w_dtype, c, n); };
     int64_t row = (int64_t)blockIdx.x * kRows + (W == 1 ? wv : 0);
-    const auto fetch = [&](int64_t r) {
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            gn[i] = load8_raw(g + r * p.ldg, c0 + i * (W * 512), n);
-            hn[i] = load8_raw(h + r * p.ldh, c0 + i * (W * 512), n);
-        }
-    };
-    if (row < p.T) fetch(row);
     for (int turn = 0; row < p.T; row += step, turn ^= 1) {
         f32x8 gv[VPT], hv[VPT];
+        Raw8<G> gr[VPT];
+        Raw8<H> hr[VPT];
+        Raw8<D> dr[VPT];
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = c0 + i * (W * 512);
+            gr[i] = fetch8(static_cast<const G *>(p.g) + row * p.ldg, c, n);
+            hr[i] = fetch8(static_cast<const H *>(p.h) + row * p.ldh, c, n);
+            // (before the first store, since it may be grad_in)
+            if (p.gh) dr[i] = fetch8(static_cast<const D *>(p.gh) + row * p.ldgh, c, n);
+        }
         float sq = 0.0f, dot = 0.0f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            gv[i] = widen(gn[i]);
-            hv[i] = widen(hn[i]);
-            const f32x8 w = load8_any(p.weight, p.w_dtype, c0 + i * (W * 512), n);
+            const int c = c0 + i * (W * 512);
+            gv[i] = settle8<G>(gr[i], c, n);
+            hv[i] = settle8<H>(hr[i], c, n);
+            const f32x8 u = gv[i] * weight(c);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 sq += hv[i][j] * hv[i][j];
-                dot += gv[i][j] * w[j] * hv[i][j];
+                dot += u[j] * hv[i][j];
             }
         }
-        if (row + step < p.T) fetch(row + step);
         sq = wave_sum(sq);
         dot = wave_sum(dot);
         if (W > 1) {
@@ -303,15 +376,12 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_grad_rows(NormGrad
         G *gi = static_cast<G *>(p.gi) + row * p.ldgi;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int64_t c = c0 + i * (W * 512);
+            const int c = c0 + i * (W * 512);
             const f32x8 nv = hv[i] * r;
             gw[i] += gv[i] * nv;
-            f32x8 d = (gv[i] * load8_any(p.weight, p.w_dtype, c, n) - nv * mean) * r;
-            if (p.gh) {
-                const char *gh = static_cast<const char *>(p.gh) + row * p.ldgh * (p.gh_dtype == EMU_DT_FP32 ? 4 : 2);
-                d += load8_any(gh, p.gh_dtype, c, n);
-            }
-            if (c < n) store8_row(gi, c, n, d);
+            f32x8 d = (gv[i] * weight(c) - nv * mean) * r;
+            if (p.gh) d += settle8<D>(dr[i], c, n);
+            store8_row(gi, c, n, d);
         }
     }
     if (W == 1) {  // the four waves' sums, in the order of the waves
@@ -332,26 +402,28 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_grad_rows(NormGrad
     float *part = p.part + (int64_t)blockIdx.x * n;
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
-        if (c0 + i * (W * 512) < n) store8_row(part, c0 + i * (W * 512), n, gw[i]);
+        store8_row(part, c0 + i * (W * 512), n, gw[i]);
 }
 
-// Rows too long for registers: the row is read twice, and the workgroup's own
+// Rows too long for registers (or of fewer than 8 values): the row is read
+// twice, and the workgroup's own
 // part in the workspace takes the place of the sums in registers.
 template <typename G, typename H>
 __global__ __launch_bounds__(1024) void norm_grad_long_rows(NormGradParams p, int64_t parts)
 {
     __shared__ float lds[2][2][16];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t n = p.n;
+    const int lane = threadIdx.x & 63, wave = wave_index();
+    const int n = (int)p.n;
     float *part = p.part + (int64_t)blockIdx.x * n;
+    const auto weight = [&](int c) { return settle8_any(fetch8_any(p.weight, p.w_dtype, c, n), p.w_dtype, c, n); };
     int turn = 0;
     bool first = true;
     for (int64_t row = blockIdx.x; row < p.T; row += parts, turn ^= 1, first = false) {
         const G *g = static_cast<const G *>(p.g) + row * p.ldg;
         const H *h = static_cast<const H *>(p.h) + row * p.ldh;
         float sq = 0.0f, dot = 0.0f;
-        for (int64_t c = threadIdx.x * 8; c < n; c += 8192) {
-            const f32x8 gv = load8_row(g, c, n), hv = load8_row(h, c, n), w = load8_any(p.weight, p.w_dtype, c, n);
+        for (int c = threadIdx.x * 8; c < n; c += 8192) {
+            const f32x8 gv = settle8<G>(fetch8(g, c, n), c, n), hv = settle8<H>(fetch8(h, c, n), c, n), w = weight(c);
             float a = 0.0f, b = 0.0f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -365,35 +437,37 @@ __global__ __launch_bounds__(1024) void norm_grad_long_rows(NormGradParams p, in
         dot = row_sum<16>(dot, lds[turn][1], wave, lane);
         const float r = 1.0f / sqrtf(sq / (float)n + p.eps);
         const float mean = dot * r / (float)n;
-        for (int64_t c = threadIdx.x * 8; c < n; c += 8192) {
-            const f32x8 gv = load8_row(g, c, n), nv = load8_row(h, c, n) * r;
-            f32x8 d = (gv * load8_any(p.weight, p.w_dtype, c, n) - nv * mean) * r;
+        for (int c = threadIdx.x * 8; c < n; c += 8192) {
+            const f32x8 gv = settle8<G>(fetch8(g, c, n), c, n), nv = settle8<H>(fetch8(h, c, n), c, n) * r;
+            f32x8 d = (gv * weight(c) - nv * mean) * r;
             if (p.gh) {
                 const char *gh = static_cast<const char *>(p.gh) + row * p.ldgh * (p.gh_dtype == EMU_DT_FP32 ? 4 : 2);
-                d += load8_any(gh, p.gh_dtype, c, n);
+                d += settle8_any(fetch8_any(gh, p.gh_dtype, c, n), p.gh_dtype, c, n);
             }
             f32x8 t = gv * nv;
-            if (!first) t += load8_row(part, c, n);
+            if (!first) t += settle8<float>(fetch8(part, c, n), c, n);
             store8_row(part, c, n, t);
             store8_row(static_cast<G *>(p.gi) + row * p.ldgi, c, n, d);
         }
     }
 }
 
-// grad_weight: 64 columns a workgroup, 16 waves that each add every 16th
-// part, joined in the order of the waves.
+// grad_weight: 32 columns a workgroup, 32 half waves that each add every 32nd
+// part, joined in the order of the half waves.
 __global__ __launch_bounds__(1024) void grad_weight_kernel(NormGradParams p, int64_t parts)
 {
-    __shared__ float lds[16][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+    __shared__ float lds[32][33];
+    const int col = threadIdx.x & 31, half = threadIdx.x >> 5;
+    int64_t c = (int64_t)blockIdx.x * 32 + col;
     float s = 0.0f;
-    if (c < p.n)
-        for (int64_t i = wave; i < parts; i += 16) s += p.part[i * p.n + c];
-    lds[wave][lane] = s;
+    if (c < p.n) {
+#pragma unroll 8
+        for (int64_t i = half; i < parts; i += 32) s += p.part[i * p.n + c];
+    }
+    lds[half][col] = s;
     __syncthreads();
-    if (wave || c >= p.n) return;
-    for (int i = 1; i < 16; ++i) s += lds[i][lane];
+    if (half || c >= p.n) return;
+    for (int i = 1; i < 32; ++i) s += lds[i][col];
     if (p.w_dtype == EMU_DT_BF16)
         static_cast<__bf16 *>(p.gw)[c] = (__bf16)s;
     else if (p.w_dtype == EMU_DT_FP16)
@@ -402,36 +476,49 @@ __global__ __launch_bounds__(1024) void grad_weight_kernel(NormGradParams p, int
         static_cast<float *>(p.gw)[c] = s;
 }
 
-template <typename G, typename H>
+template <typename G, typename H, typename D>
 void launch_norm_grad_of(const NormGradParams &p, int64_t parts, hipStream_t stream)
 {
     const int64_t n = p.n;
     const dim3 grid((unsigned)parts);
-    if (n <= 512)
-        hipLaunchKernelGGL((norm_grad_rows<G, H, 1, 1>), grid, dim3(256), 0, stream, p, parts);
-    else if (n <= 1024)
-        hipLaunchKernelGGL((norm_grad_rows<G, H, 1, 2>), grid, dim3(256), 0, stream, p, parts);
-    else if (n <= 2048)
-        hipLaunchKernelGGL((norm_grad_rows<G, H, 4, 1>), grid, dim3(256), 0, stream, p, parts);
-    else if (n <= 4096)
-        hipLaunchKernelGGL((norm_grad_rows<G, H, 8, 1>), grid, dim3(512), 0, stream, p, parts);
-    else if (n <= 8192)
-        hipLaunchKernelGGL((norm_grad_rows<G, H, 8, 2>), grid, dim3(512), 0, stream, p, parts);
-    else if (n <= 16384)
-        hipLaunchKernelGGL((norm_grad_rows<G, H, 16, 2>), grid, dim3(1024), 0, stream, p, parts);
-    else
+    if (n < 8 || n > 16384)
         hipLaunchKernelGGL((norm_grad_long_rows<G, H>), grid, dim3(1024), 0, stream, p, parts);
+    else if (n <= 512)
+        hipLaunchKernelGGL((norm_grad_rows<G, H, D, 1, 1>), grid, dim3(256), 0, stream, p, parts);
+    else if (n <= 1024)
+        hipLaunchKernelGGL((norm_grad_rows<G, H, D, 1, 2>), grid, dim3(256), 0, stream, p, parts);
+    else if (n <= 2048)
+        hipLaunchKernelGGL((norm_grad_rows<G, H, D, 4, 1>), grid, dim3(256), 0, stream, p, parts);
+    else if (n <= 4096)
+        hipLaunchKernelGGL((norm_grad_rows<G, H, D, 8, 1>), grid, dim3(512), 0, stream, p, parts);
+    else if (n <= 8192)
+        hipLaunchKernelGGL((norm_grad_rows<G, H, D, 8, 2>), grid, dim3(512), 0, stream, p, parts);
+    else
+        hipLaunchKernelGGL((norm_grad_rows<G, H, D, 16, 2>), grid, dim3(1024), 0, stream, p, parts);
+}
+
+template <typename G, typename H>
+void launch_norm_grad_gh(const NormGradParams &p, int64_t parts, hipStream_t stream)
+{
+    if (p.gh && p.gh_dtype == EMU_DT_FP32)
+        launch_norm_grad_of<G, H, float>(p, parts, stream);
+    else
+        launch_norm_grad_of<G, H, G>(p, parts, stream);
 }
 
 }  // namespace
 
 // Workgroups of the gradient, each with a part of grad_weight in the
-// workspace: at most two for each CU, and one for each row (or four rows of
-// up to 1,024 values, a row to a wave).
+// workspace: 16 waves for each CU, but over 512 only where each gets 8 rows
+// (8192 x 2048: 25 us with 1024 parts, 30 with 512; 1023 x 1925, both kernels:
+// 17 and 13 us), and one for each row (or four rows of up to 1,024 values, a
+// row to a wave).
 int64_t norm_grad_parts(int64_t T, int64_t n)
 {
-    const int64_t most = n <= 1024 ? (T + 3) / 4 : T;
-    return most < 512 ? most : 512;
+    const int64_t most = n >= 8 && n <= 1024 ? (T + 3) / 4 : T;
+    int64_t parts = n <= 2048 ? 1024 : n <= 8192 ? 512 : 256;
+    if (parts > 512 && parts > T / 8) parts = T / 8 > 512 ? T / 8 : 512;
+    return most < parts ? most : parts;
 }
 
 hipError_t launch_norm_grad(int g_dtype, int h_dtype, const NormGradParams &p, hipStream_t stream)
@@ -439,19 +526,19 @@ hipError_t launch_norm_grad(int g_dtype, int h_dtype, const NormGradParams &p, h
     const int64_t parts = norm_grad_parts(p.T, p.n);
     if (parts > 0) {
         if (g_dtype == EMU_DT_FP32)
-            launch_norm_grad_of<float, float>(p, parts, stream);
+            launch_norm_grad_gh<float, float>(p, parts, stream);
         else if (g_dtype == EMU_DT_BF16 && h_dtype == EMU_DT_FP32)
-            launch_norm_grad_of<__bf16, float>(p, parts, stream);
+            launch_norm_grad_gh<__bf16, float>(p, parts, stream);
         else if (g_dtype == EMU_DT_BF16)
-            launch_norm_grad_of<__bf16, __bf16>(p, parts, stream);
+            launch_norm_grad_gh<__bf16, __bf16>(p, parts, stream);
         else if (h_dtype == EMU_DT_FP32)
-            launch_norm_grad_of<_Float16, float>(p, parts, stream);
+            launch_norm_grad_gh<_Float16, float>(p, parts, stream);
         else
-            launch_norm_grad_of<_Float16, _Float16>(p, parts, stream);
+            launch_norm_grad_gh<_Float16, _Float16>(p, parts, stream);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL(grad_weight_kernel, dim3((unsigned)((p.n + 63) / 64)), dim3(1024), 0, stream, p, parts);
+    hipLaunchKernelGGL(grad_weight_kernel, dim3((unsigned)((p.n + 31) / 32)), dim3(1024), 0, stream, p, parts);
     return hipGetLastError();
 }
 

@@ -10,75 +10,131 @@ namespace emu {
 
 typedef float f32x8 __attribute__((ext_vector_type(8)));
 
+// The index of this thread's wave in its workgroup, known to be the same for all its lanes.
+__device__ __forceinline__ int wave_index() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
 // An element type and its vector of 8.  Rows start where the caller's
 // leading dimension puts them, so vectors are accessed with the element's
 // alignment only: the GPU runs in unaligned-access mode, where the same
-// 16-byte instructions serve both.
+// 16-byte instructions serve both (512 MiB: loads 6.5 TB/s aligned to 4
+// bytes, 4.6 to 2; stores 4.3 and 3.4).
 template <typename E>
 struct Vec8 {
     typedef E type __attribute__((ext_vector_type(8)));
     typedef type mem __attribute__((aligned(sizeof(E))));
 };
+template <typename E>
+using Raw8 = typename Vec8<E>::type;
 
 template <typename E>
-__device__ __forceinline__ f32x8 load8(const E *p)
+__device__ __forceinline__ Raw8<E> load8(const E *p)
 {
-    const typename Vec8<E>::type v = *reinterpret_cast<const typename Vec8<E>::mem *>(p);
+    return *reinterpret_cast<const typename Vec8<E>::mem *>(p);
+}
+template <typename E>
+__device__ __forceinline__ f32x8 widen(const Raw8<E> &v)
+{
     return __builtin_convertvector(v, f32x8);
 }
 
-// The first `valid` (0..8) of 8 elements; the rest are `fill`.
-template <typename E>
-__device__ __forceinline__ f32x8 load8_part(const E *p, int valid, float fill = 0.0f)
+// Moves v down by k (0..8) elements, zeros after.
+__device__ __forceinline__ f32x8 moved(f32x8 v, int k)
 {
-    f32x8 r;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = i < valid ? (float)p[i] : fill;
-    return r;
+    if (k & 1) v = f32x8{v[1], v[2], v[3], v[4], v[5], v[6], v[7], 0.0f};
+    if (k & 2) v = f32x8{v[2], v[3], v[4], v[5], v[6], v[7], 0.0f, 0.0f};
+    if (k & 4) v = f32x8{v[4], v[5], v[6], v[7], 0.0f, 0.0f, 0.0f, 0.0f};
+    if (k & 8) v = 0.0f;
+    return v;
 }
 
-// As stored, for values that wait in registers before they are used.
+// Elements c .. c + 7 of a row of n in two steps, so that all of a lane's
+// loads are under way before the first is used: fetch8 reads them, or, where
+// the row ends before, its last eight, with the same instruction; settle8
+// then moves those into place, zeros past the end.
 template <typename E>
-__device__ __forceinline__ typename Vec8<E>::type load8_raw(const E *row, int64_t c, int64_t n)
+__device__ __forceinline__ Raw8<E> fetch8(const E *row, int c, int n)
 {
-    if (c + 8 <= n) return *reinterpret_cast<const typename Vec8<E>::mem *>(row + c);
-    typename Vec8<E>::type r;
+    if (n >= 8) return load8(row + (c + 8 <= n ? c : n - 8));
+    Raw8<E> r;
 #pragma unroll
     for (int i = 0; i < 8; ++i) r[i] = c + i < n ? row[c + i] : (E)0.0f;
     return r;
 }
-
-template <typename E>
-__device__ __forceinline__ f32x8 load8_row(const E *row, int64_t c, int64_t n, float fill = 0.0f)
+__device__ __forceinline__ f32x8 settled(const f32x8 &v, int c, int n)
 {
-    if (c + 8 <= n) return load8(row + c);
-    return load8_part(row + c, c < n ? (int)(n - c) : 0, fill);
+    if (n < 8 || c + 8 <= n) return v;
+    return moved(v, c + 8 - n < 8 ? c + 8 - n : 8);
+}
+template <typename E>
+__device__ __forceinline__ f32x8 settle8(const Raw8<E> &raw, int c, int n)
+{
+    return settled(widen<E>(raw), c, n);
 }
 
-// The same with the type known at run time only (uniform over the launch).
-__device__ __forceinline__ f32x8 load8_any(const void *row, int dtype, int64_t c, int64_t n)
+// The same where the type is known at run time only (uniform over the launch).
+struct AnyRaw8 {
+    Raw8<float> v;  // binary32, or 8 elements of 16 bits in the first half
+};
+__device__ __forceinline__ AnyRaw8 fetch8_any(const void *row, int dtype, int c, int n)
 {
-    if (dtype == EMU_DT_BF16) return load8_row(static_cast<const __bf16 *>(row), c, n);
-    if (dtype == EMU_DT_FP16) return load8_row(static_cast<const _Float16 *>(row), c, n);
-    return load8_row(static_cast<const float *>(row), c, n);
-}
-
-template <typename E>
-__device__ __forceinline__ void store8_row(E *row, int64_t c, int64_t n, const f32x8 &v)
-{
-    const typename Vec8<E>::type r = __builtin_convertvector(v, typename Vec8<E>::type);
-    if (c + 8 <= n) {
-        *reinterpret_cast<typename Vec8<E>::mem *>(row + c) = r;
+    if (dtype == EMU_DT_FP32) return AnyRaw8{fetch8(static_cast<const float *>(row), c, n)};
+    typedef float f32x4 __attribute__((ext_vector_type(4)));
+    typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
+    u16x8 h;
+    const uint16_t *r = static_cast<const uint16_t *>(row);
+    if (n >= 8) {
+        typedef u16x8 mem __attribute__((aligned(2)));
+        h = *reinterpret_cast<const mem *>(r + (c + 8 <= n ? c : n - 8));
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (c + i < n) row[c + i] = r[i];
+        for (int i = 0; i < 8; ++i) h[i] = c + i < n ? r[c + i] : (uint16_t)0;
     }
+    const f32x4 q = __builtin_bit_cast(f32x4, h);
+    return AnyRaw8{f32x8{q[0], q[1], q[2], q[3], 0.0f, 0.0f, 0.0f, 0.0f}};
+}
+__device__ __forceinline__ f32x8 settle8_any(const AnyRaw8 &raw, int dtype, int c, int n)
+{
+    f32x8 v = raw.v;
+    if (dtype != EMU_DT_FP32) {
+        typedef float f32x4 __attribute__((ext_vector_type(4)));
+        const f32x4 q = {v[0], v[1], v[2], v[3]};
+        v = dtype == EMU_DT_BF16 ? widen<__bf16>(__builtin_bit_cast(Raw8<__bf16>, q))
+                                 : widen<_Float16>(__builtin_bit_cast(Raw8<_Float16>, q));
+    }
+    return settled(v, c, n);
+}
+
+// Elements c .. c + 7, those past n (or all of them) not stored; past the end in pieces of 4, 2 and 1.
+template <typename E>
+__device__ __forceinline__ void store8_row(E *row, int c, int n, f32x8 v)
+{
+    E *p = row + c;
+    if (c + 8 <= n) {
+        *reinterpret_cast<typename Vec8<E>::mem *>(p) = __builtin_convertvector(v, Raw8<E>);
+        return;
+    }
+    const int left = c < n ? n - c : 0;
+    if (left & 4) {
+        typedef E e4 __attribute__((ext_vector_type(4)));
+        typedef e4 mem __attribute__((aligned(sizeof(E))));
+        *reinterpret_cast<mem *>(p) = e4{(E)v[0], (E)v[1], (E)v[2], (E)v[3]};
+        p += 4;
+        v = moved(v, 4);
+    }
+    if (left & 2) {
+        typedef E e2 __attribute__((ext_vector_type(2)));
+        typedef e2 mem __attribute__((aligned(sizeof(E))));
+        *reinterpret_cast<mem *>(p) = e2{(E)v[0], (E)v[1]};
+        p += 2;
+        v = moved(v, 2);
+    }
+    if (left & 1) *p = (E)v[0];
 }
 
 // Reductions over a wave's 64 lanes; every lane gets the result, the same
 // bits in each (the butterfly's sums are symmetric).
-__device__ __forceinline__ float wave_sum(float v)
+template <typename T>
+__device__ __forceinline__ T wave_sum(T v)
 {
 #pragma unroll
     for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
@@ -94,14 +150,14 @@ __device__ __forceinline__ float wave_max(float v)
 
 // Over the W waves of a row, through W words of LDS; W = 1 needs neither LDS
 // nor a barrier.  Two reductions in a row need two arrays.
-template <int W>
-__device__ __forceinline__ float row_sum(float v, float *lds, int wave, int lane)
+template <int W, typename T>
+__device__ __forceinline__ T row_sum(T v, T *lds, int wave, int lane)
 {
     v = wave_sum(v);
     if (W == 1) return v;
     if (lane == 0) lds[wave] = v;
     __syncthreads();
-    float s = lds[0];
+    T s = lds[0];
 #pragma unroll
     for (int i = 1; i < W; ++i) s += lds[i];
     return s;
