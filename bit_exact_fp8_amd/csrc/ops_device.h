@@ -37,13 +37,13 @@ __device__ __forceinline__ f32x8 widen(const Raw8<E> &v)
     return __builtin_convertvector(v, f32x8);
 }
 
-// Moves v down by k (0..8) elements, zeros after.
-__device__ __forceinline__ f32x8 moved(f32x8 v, int k)
+// Moves v down by k (0..8) elements, `fill` after.
+__device__ __forceinline__ f32x8 moved(f32x8 v, int k, float fill = 0.0f)
 {
-    if (k & 1) v = f32x8{v[1], v[2], v[3], v[4], v[5], v[6], v[7], 0.0f};
-    if (k & 2) v = f32x8{v[2], v[3], v[4], v[5], v[6], v[7], 0.0f, 0.0f};
-    if (k & 4) v = f32x8{v[4], v[5], v[6], v[7], 0.0f, 0.0f, 0.0f, 0.0f};
-    if (k & 8) v = 0.0f;
+    if (k & 1) v = f32x8{v[1], v[2], v[3], v[4], v[5], v[6], v[7], fill};
+    if (k & 2) v = f32x8{v[2], v[3], v[4], v[5], v[6], v[7], fill, fill};
+    if (k & 4) v = f32x8{v[4], v[5], v[6], v[7], fill, fill, fill, fill};
+    if (k & 8) v = fill;
     return v;
 }
 
@@ -131,21 +131,48 @@ __device__ __forceinline__ void store8_row(E *row, int c, int n, f32x8 v)
     if (left & 1) *p = (E)v[0];
 }
 
-// Reductions over a wave's 64 lanes; every lane gets the result, the same
-// bits in each (the butterfly's sums are symmetric).
+// Reductions over a wave's 64 lanes, all of them active; every lane gets the
+// result, the same bits in each (f(a, b) and f(b, a) are the same).  Lanes
+// 1, 2, 4 and 8 apart meet by DPP (the mirrors do for 4 and 8 once the lanes
+// between agree), rows of 16 and halves by swaps: no step goes through LDS.
+template <typename T, typename F>
+__device__ __forceinline__ T by_words(const T &v, F f)
+{
+    constexpr int N = sizeof(T) / 4;
+    struct Words {
+        uint32_t w[N];
+    };
+    Words x = __builtin_bit_cast(Words, v);
+#pragma unroll
+    for (int i = 0; i < N; ++i) x.w[i] = f(x.w[i]);
+    return __builtin_bit_cast(T, x);
+}
+template <int CTRL, typename T>
+__device__ __forceinline__ T by_dpp(const T &v)
+{
+    return by_words(v, [](uint32_t w) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)w, CTRL, 0xF, 0xF, true); });
+}
+template <typename T, typename F>
+__device__ __forceinline__ T wave_reduce(T v, F f)
+{
+    v = f(v, by_dpp<0xB1>(v));   // quad_perm 1 0 3 2
+    v = f(v, by_dpp<0x4E>(v));   // quad_perm 2 3 0 1
+    v = f(v, by_dpp<0x141>(v));  // row_half_mirror
+    v = f(v, by_dpp<0x140>(v));  // row_mirror
+    v = f(by_words(v, [](uint32_t w) { return (uint32_t)__builtin_amdgcn_permlane16_swap(w, w, false, false)[0]; }),
+          by_words(v, [](uint32_t w) { return (uint32_t)__builtin_amdgcn_permlane16_swap(w, w, false, false)[1]; }));
+    return f(by_words(v, [](uint32_t w) { return (uint32_t)__builtin_amdgcn_permlane32_swap(w, w, false, false)[0]; }),
+             by_words(v, [](uint32_t w) { return (uint32_t)__builtin_amdgcn_permlane32_swap(w, w, false, false)[1]; }));
+}
 template <typename T>
 __device__ __forceinline__ T wave_sum(T v)
 {
-#pragma unroll
-    for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
-    return v;
+    return wave_reduce(v, [](T a, T b) { return a + b; });
 }
 // A NaN in any lane wins.
 __device__ __forceinline__ float wave_max(float v)
 {
-#pragma unroll
-    for (int o = 32; o; o >>= 1) v = __builtin_elementwise_maximum(v, __shfl_xor(v, o));
-    return v;
+    return wave_reduce(v, [](float a, float b) { return __builtin_elementwise_maximum(a, b); });
 }
 
 // Over the W waves of a row, through W words of LDS; W = 1 needs neither LDS
