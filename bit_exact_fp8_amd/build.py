@@ -58,7 +58,7 @@ def _run(cmd, verbose):
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(" ".join(cmd) + "\n" + res.stdout + res.stderr)
-        raise RuntimeError("hipcc failed to build libemu_fp8gemm.so")
+        raise RuntimeError(f"{cmd[0]} failed: {cmd[-1]} is not built")
 
 
 def build(output: str = OUTPUT, extra_flags=None, verbose: bool = False, jobs: int | None = None) -> str:
@@ -70,6 +70,26 @@ def build(output: str = OUTPUT, extra_flags=None, verbose: bool = False, jobs: i
             list(ex.map(lambda c: _run(c, verbose), cmds))
         tmp = output + ".tmp"
         _run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *[obj for _, obj, _ in units], "-o", tmp], verbose)
+    os.replace(tmp, output)
+    return output
+
+
+BINDING_OUTPUT = os.path.join(PKG, "_ops.so")
+
+
+def build_binding(output: str = BINDING_OUTPUT, verbose: bool = False) -> str:
+    """The operators' Python calls (ops_binding.cpp), host code against torch's C++ interface."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    includes = [sysconfig.get_paths()["include"], *cpp_extension.include_paths(), "/opt/rocm/include",
+                os.path.join(ROOT, "include")]
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = output + ".tmp"
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", *[f"-isystem{d}" for d in includes],
+          os.path.join(CSRC, "ops_binding.cpp"), f"-L{libs}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip", "-o", tmp], verbose)
     os.replace(tmp, output)
     return output
 
@@ -87,4 +107,5 @@ def build_microbench(output: str = MICROBENCH_OUTPUT, verbose: bool = False) -> 
 
 if __name__ == "__main__":
     print(build(verbose=True))
+    print(build_binding(verbose=True))
     print(build_microbench(verbose=True))

@@ -795,3 +795,31 @@ def test_int8_mm_wide_rows(dev):
     sa = torch.full((1,), 0.01, device=dev)
     y = fw.int8_scaled_mm(big[:, 64:576], w.to(dev).t(), sa, sa, out_dtype=SF)
     assert torch.equal(y.cpu(), mm_want(a, w, sa.cpu(), sa.cpu(), None, SF))
+
+
+@pytest.mark.gpu
+def test_leading_axes_and_argument_types(dev):
+    """Rows of several axes are one axis of rows with one stride, or refused;
+    arguments of other kinds are refused by name."""
+    base = torch.zeros(4, 6, 64, device=dev)
+    w = torch.ones(64, device=dev)
+    for x in (base, base[:, :1], base[1:2], base.view(2, 2, 6, 64), base[::2, 0], base[:0], base[:, 3]):
+        codes, scale, _ = fw.add_rms_norm_quant(x, w)
+        assert codes.shape == x.shape and scale.shape == x.shape[:-1] + (1,)
+    for x in (base[:, :3], base.transpose(0, 1), base[::2, ::2]):
+        with pytest.raises(ValueError, match="one axis of rows"):
+            fw.add_rms_norm_quant(x, w)
+    with pytest.raises(ValueError, match="at least one axis"):
+        fw.add_rms_norm_quant(w[0], w)
+    tok = torch.zeros(4, dtype=torch.int64, device=dev)
+    for bad in (lambda: fw.add_rms_norm_quant(base, 1.0), lambda: fw.add_rms_norm_quant(base, w, eps="small"),
+                lambda: fw.token_logprobs(base[0], [0] * 6), lambda: fw.token_logprobs(base[0, :4], tok, top_k=1.5),
+                lambda: fw.int8_scaled_mm(None, None, w, w)):
+        with pytest.raises(TypeError):
+            bad()
+    with pytest.raises(fw.EmuError) as e:
+        fw.token_logprobs(base[0, :4], tok, top_k=-1)
+    assert e.value.status == 1
+    with pytest.raises(fw.EmuError) as e:
+        fw.add_rms_norm_quant(base, w, out_dtype="int8")
+    assert e.value.status == 3
