@@ -98,11 +98,11 @@ __device__ __forceinline__ void take16(Run &a, f32x8 x, f32x8 y, float most)
     a.u += u[0] + u[1];
 }
 
-__device__ __forceinline__ float most16(const f32x8 &x, const f32x8 &y)
+__device__ __forceinline__ float most8(const f32x8 &x)
 {
-    float m = __builtin_elementwise_maximum(x[0], y[0]);
+    float m = x[0];
 #pragma unroll
-    for (int j = 1; j < 8; ++j) m = __builtin_elementwise_maximum(__builtin_elementwise_maximum(m, x[j]), y[j]);
+    for (int j = 1; j < 8; ++j) m = __builtin_elementwise_maximum(m, x[j]);
     return m;
 }
 
@@ -315,33 +315,44 @@ __device__ __forceinline__ void rank_candidates(const TopShared &sh, int count, 
     }
 }
 
+// What a thread knows of its logits.
+struct Own {
+    uint64_t key;  // a lower bound for its largest key (that of its vector's last index), or 0
+    int at;        // that vector's first index
+    float second;  // the largest logit of its other vectors
+};
+
 // The k largest keys of the segment [s0, s1), in falling order; fewer where
-// it has fewer logits, and zeros for the rest.  emit(i, key).  `mine`: a lower
-// bound for this thread's largest key, or 0.  HELD: the segment's logits
-// are x (from s0 + 8 threadIdx.x) and y (a tile further); else they are read again.
+// it has fewer logits, and zeros for the rest.  emit(i, key).  HELD: the
+// segment's logits are x (from s0 + 8 threadIdx.x) and y (a tile further);
+// else a thread whose key passes reads its vector again, and where its others
+// may hold a logit that passes, all threads read those.
 template <bool HELD, typename Z, typename Emit>
 __device__ __forceinline__ void top_of_segment(const Z *z, int s0, int s1, const f32x8 &x, const f32x8 &y, int k,
-                                               uint64_t mine, TopShared &sh, Emit emit)
+                                               const Own &own, TopShared &sh, Emit emit)
 {
     const int t = threadIdx.x;
-    sh.key[t] = mine;
+    sh.key[t] = own.key;
     clear(sh);
     __syncthreads();
     uint64_t all[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) all[i] = sh.key[i * 64 + (t & 63)];
     const uint64_t bound = kth_key<kOrderBits<Z>>(all, k);  // the same in every wave
+    const bool wins = own.key && own.key >= bound;
+    const float least = bound ? unordered((uint32_t)(bound >> 32)) : -INFINITY;
+    const bool others = wins && own.second >= least;
     if (!HELD) {
-        if (mine && mine >= bound) sh.winner[atomicAdd(&sh.winners, 1)] = (uint16_t)t;
+        if (others) sh.winner[atomicAdd(&sh.winners, 1)] = (uint16_t)t;
         __syncthreads();
     }
-    const float least = bound ? unordered((uint32_t)(bound >> 32)) : -INFINITY;
     const auto each = [&](auto f) {  // f(vector, its first index), of all that may hold a logit that passes
         if constexpr (HELD) {
-            if (!mine || mine < bound) return;
+            if (!wins) return;
             f(x, s0 + t * 8);
             f(y, s0 + t * 8 + kTile);
         } else {
+            if (wins && !others) f(logits8(z, own.at, s1), own.at);
             const int winners = sh.winners, iters = (s1 - s0 + kTile - 1) / kTile;
             for (int j = t; j < winners * iters; j += kThreads) {
                 const int c = s0 + j / winners * kTile + (int)sh.winner[j % winners] * 8;
@@ -350,7 +361,7 @@ __device__ __forceinline__ void top_of_segment(const Z *z, int s0, int s1, const
         }
     };
     each([&](const f32x8 &v, int c) {
-        if (most16(v, v) < least || c >= s1) return;
+        if (most8(v) < least || c >= s1) return;
         const int at = atomicAdd(&sh.vectors, 1);
         if (at >= kVectors) return;
         *reinterpret_cast<f32x8 *>(sh.logit[at]) = v;
@@ -397,7 +408,7 @@ __device__ __forceinline__ void top_of_segment(const Z *z, int s0, int s1, const
 // Workgroup (t, seg) of a grid of T * P: `span` logits of row t from seg * span.
 // With P = 1 it finishes the row; else logp_join does.  HELD: span is at
 // most two tiles, which stay in registers.
-template <typename Z, bool TOP, bool HELD>
+template <typename Z, bool TOP, bool HELD, bool ONCE>
 __global__ __launch_bounds__(kThreads, HELD ? 6 : 8) void logp_rows(LogpParams p, int64_t first_row, int P, int span)
 {
     __shared__ Run waves[4];
@@ -412,15 +423,14 @@ __global__ __launch_bounds__(kThreads, HELD ? 6 : 8) void logp_rows(LogpParams p
     if (P == 1) logit = token_logit(p, z, t, threadIdx.x, token);
 
     Run a = empty_run();
-    int at = -1;  // where this thread's largest logit was first met
+    int at = -1;  // the vector where this thread's largest logit was first met
+    float second = -INFINITY;  // the largest logit of its other vectors
     const int c0 = s0 + (int)threadIdx.x * 8;
     const auto take = [&](const f32x8 &x, const f32x8 &y, int c) {
-        const float most = most16(x, y);
-        if (TOP && most > a.most) {
-            bool first = false;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) first |= x[j] == most;
-            at = first ? c : c + kTile;
+        const float mx = most8(x), my = most8(y), most = __builtin_elementwise_maximum(mx, my);
+        if (TOP) {
+            second = fmaxf(second, fmaxf(fminf(mx, my), fminf(most, a.most)));
+            if (most > a.most) at = mx == most ? c : c + kTile;
         }
         take16(a, x, y, most);
     };
@@ -431,16 +441,12 @@ __global__ __launch_bounds__(kThreads, HELD ? 6 : 8) void logp_rows(LogpParams p
         take(x, y, c0);
     } else {
         int c = c0;
-        for (; c + kTile + 8 <= s1; c += 2 * kTile) take(widen<Z>(load8(z + c)), widen<Z>(load8(z + c + kTile)), c);
+        for (; c + kTile + 8 <= s1; c += 2 * kTile) take(widen<Z>(load8<ONCE>(z + c)), widen<Z>(load8<ONCE>(z + c + kTile)), c);
         if (c < s1) take(logits8(z, c, s1), logits8(z, c + kTile, s1), c);
     }
 
-    uint64_t mine = 0;
-    if (TOP && c0 < s1) {
-        // a lower bound for the key of this thread's largest logit: its vector's last index
-        const int from = at < 0 ? c0 : at;
-        mine = key_of(at < 0 ? -INFINITY : a.most, (uint32_t)(from + 7));
-    }
+    Own own{0, at < 0 ? c0 : at, second};
+    if (TOP && c0 < s1) own.key = key_of(a.most, (uint32_t)(own.at + 7));
     a = block_join(a, waves);
     Stats st{a.most, 0.0f, 0.0f};
     if (a.most == -INFINITY)
@@ -465,7 +471,7 @@ __global__ __launch_bounds__(kThreads, HELD ? 6 : 8) void logp_rows(LogpParams p
             if (r.nan)
                 write_no_top(p, t);
             else
-                top_of_segment<HELD>(z, s0, s1, x, y, p.k, mine, sh,
+                top_of_segment<HELD>(z, s0, s1, x, y, p.k, own, sh,
                                      [&](int i, uint64_t key) { write_top(p, t, i, key, r.lse); });
         }
         return;
@@ -474,7 +480,7 @@ __global__ __launch_bounds__(kThreads, HELD ? 6 : 8) void logp_rows(LogpParams p
     if (threadIdx.x == 0) stats[t * P + seg] = make_float4(st.m, st.s, st.u, 0.0f);
     if (TOP && st.m == st.m) {
         uint64_t *keys = reinterpret_cast<uint64_t *>(stats + p.T * P) + (t * P + seg) * p.k;
-        top_of_segment<HELD>(z, s0, s1, x, y, p.k, mine, sh, [&](int i, uint64_t key) { keys[i] = key; });
+        top_of_segment<HELD>(z, s0, s1, x, y, p.k, own, sh, [&](int i, uint64_t key) { keys[i] = key; });
     }
 }
 
@@ -561,10 +567,10 @@ Split split_of(int64_t T, int64_t V, int k)
 
 constexpr int64_t kRowsPerLaunch = 1 << 20;  // grid x threads stays below 2^32
 
-template <typename Z, bool TOP, bool HELD>
+template <typename Z, bool TOP, bool HELD, bool ONCE>
 void launch_rows(const LogpParams &p, int64_t r, int64_t rows, const Split &s, hipStream_t stream)
 {
-    hipLaunchKernelGGL((logp_rows<Z, TOP, HELD>), dim3((unsigned)(rows * s.P)), dim3(kThreads), 0, stream, p, r, s.P, s.span);
+    hipLaunchKernelGGL((logp_rows<Z, TOP, HELD, ONCE>), dim3((unsigned)(rows * s.P)), dim3(kThreads), 0, stream, p, r, s.P, s.span);
 }
 
 template <typename Z>
@@ -572,16 +578,23 @@ hipError_t launch_logp_of(const LogpParams &p, hipStream_t stream)
 {
     const Split s = split_of(p.T, p.V, p.k);
     const bool held = s.span <= 2 * kTile;
+    // After their producer has written them, 4096 x 65536 bf16 take 96 us past
+    // the cache and 126 through it, 1000 x 32000, which fit it, 16 and 14.
+    const bool once = p.T * p.V * (int64_t)sizeof(Z) > kOnceBytes;
     for (int64_t r = 0; r < p.T; r += kRowsPerLaunch) {
         const int64_t rows = p.T - r < kRowsPerLaunch ? p.T - r : kRowsPerLaunch;
         if (p.k && held)
-            launch_rows<Z, true, true>(p, r, rows, s, stream);
+            launch_rows<Z, true, true, false>(p, r, rows, s, stream);
+        else if (p.k && once)
+            launch_rows<Z, true, false, true>(p, r, rows, s, stream);
         else if (p.k)
-            launch_rows<Z, true, false>(p, r, rows, s, stream);
+            launch_rows<Z, true, false, false>(p, r, rows, s, stream);
         else if (held)
-            launch_rows<Z, false, true>(p, r, rows, s, stream);
+            launch_rows<Z, false, true, false>(p, r, rows, s, stream);
+        else if (once)
+            launch_rows<Z, false, false, true>(p, r, rows, s, stream);
         else
-            launch_rows<Z, false, false>(p, r, rows, s, stream);
+            launch_rows<Z, false, false, false>(p, r, rows, s, stream);
         if (s.P > 1) hipLaunchKernelGGL((logp_join<Z>), dim3((unsigned)rows), dim3(kThreads), 0, stream, p, r, s.P);
     }
     return hipGetLastError();
@@ -594,7 +607,7 @@ hipError_t launch_logp_of(const LogpParams &p, hipStream_t stream)
 // tokens' own gradients are added before the rounding.  A workgroup reads its
 // tokens' logits before it writes (grad may be the logits), and writes those
 // elements again at the end, each by the thread of the token's first mention.
-template <typename Z>
+template <typename Z, bool ONCE>
 __global__ __launch_bounds__(kThreads) void logp_grad_rows(LogpGradParams p, int64_t first_row, int64_t P, int64_t span)
 {
     extern __shared__ char dyn[];
@@ -634,11 +647,11 @@ __global__ __launch_bounds__(kThreads) void logp_grad_rows(LogpGradParams p, int
     };
     if (H) __syncthreads();
     for (int64_t c = s0 + threadIdx.x * 8; c < s1; c += kTile) {
-        const f32x8 x = settle8<Z>(fetch8(z, (int)c, (int)s1), (int)c, (int)s1);
+        const f32x8 x = settle8<Z>(fetch8<ONCE>(z, (int)c, (int)s1), (int)c, (int)s1);
         f32x8 r;
 #pragma unroll
         for (int j = 0; j < 8; ++j) r[j] = empty ? 0.0f : value(x[j]);
-        store8_row(grad + s0, (int)(c - s0), (int)(s1 - s0), r);
+        store8_row<ONCE>(grad + s0, (int)(c - s0), (int)(s1 - s0), r);
     }
     if (!H || empty) return;
     __syncthreads();
@@ -661,10 +674,17 @@ hipError_t launch_logp_grad_of(const LogpGradParams &p, hipStream_t stream)
     const int64_t span = 4 * kTile;
     const int64_t P = (p.V + span - 1) / span;
     const size_t lds = (size_t)(p.C + p.k) * 12;
+    // (as in launch_logp_of: 4096 x 65536 bf16 163 us past the cache and 187
+    // through it, 1000 x 32000 both 22)
+    const bool once = 2 * p.T * p.V * (int64_t)sizeof(Z) > kOnceBytes;
     const int64_t at_once = (int64_t(1) << 23) / P > 0 ? (int64_t(1) << 23) / P : 1;
     for (int64_t r = 0; r < p.T; r += at_once) {
         const int64_t rows = p.T - r < at_once ? p.T - r : at_once;
-        hipLaunchKernelGGL((logp_grad_rows<Z>), dim3((unsigned)(rows * P)), dim3(kThreads), lds, stream, p, r, P, span);
+        const dim3 grid((unsigned)(rows * P));
+        if (once)
+            hipLaunchKernelGGL((logp_grad_rows<Z, true>), grid, dim3(kThreads), lds, stream, p, r, P, span);
+        else
+            hipLaunchKernelGGL((logp_grad_rows<Z, false>), grid, dim3(kThreads), lds, stream, p, r, P, span);
     }
     return hipGetLastError();
 }

@@ -3,8 +3,7 @@
 // Forward: v = x + residual, y = v r w with r = 1 / sqrt(mean(v^2) + eps),
 // codes of y / scale.  Each value is needed three times (for the mean, for
 // the row's largest |y|, for its code), so a row is held in registers and
-// read once.  16384 x 8192 bf16: 162 us with a given scale, 5.8 TB/s; with
-// each row's own, which adds a reduction and a pass over the registers, 180.
+// read once.  16384 x 8192 bf16: 155 us, 6.0 TB/s.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -93,12 +92,16 @@ struct Bytes {
     T v;
 } __attribute__((packed, aligned(1)));
 
+template <bool ONCE = false>
 __device__ __forceinline__ void store_codes(uint8_t *row, int c, int n, const uint2 &r)
 {
     uint64_t v = (uint64_t)r.y << 32 | r.x;
     uint8_t *p = row + c;
     if (c + 8 <= n) {
-        reinterpret_cast<Bytes<uint64_t> *>(p)->v = v;
+        if (ONCE)
+            __builtin_nontemporal_store(v, &reinterpret_cast<Bytes<uint64_t> *>(p)->v);
+        else
+            reinterpret_cast<Bytes<uint64_t> *>(p)->v = v;
         return;
     }
     const int left = c < n ? n - c : 0;
@@ -156,12 +159,14 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_rows(NormParams p)
     {
         Raw8<X> xr[VPT];
         Raw8<std::conditional_t<kRes, R, X>> rr[VPT];
+        with_bool(p.once, [&](auto once) {
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int c = c0 + i * (W * 512);
-            xr[i] = fetch8(x, c, n);
-            if constexpr (kRes) rr[i] = fetch8(static_cast<const R *>(p.res) + row * p.ldres, c, n);
-        }
+            for (int i = 0; i < VPT; ++i) {
+                const int c = c0 + i * (W * 512);
+                xr[i] = fetch8<once()>(x, c, n);
+                if constexpr (kRes) rr[i] = fetch8<once()>(static_cast<const R *>(p.res) + row * p.ldres, c, n);
+            }
+        });
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int c = c0 + i * (W * 512);
@@ -180,8 +185,10 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_rows(NormParams p)
     if constexpr (kRes) {
         if (p.h) {
             R *h = static_cast<R *>(p.h) + row * p.ldh;
+            with_bool(p.once, [&](auto once) {
 #pragma unroll
-            for (int i = 0; i < VPT; ++i) store8_row(h, c0 + i * (W * 512), n, v[i]);
+                for (int i = 0; i < VPT; ++i) store8_row<once()>(h, c0 + i * (W * 512), n, v[i]);
+            });
         }
     }
     Factor f = factor_of(r);
@@ -207,7 +214,9 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_rows(NormParams p)
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int c = c0 + i * (W * 512);
-        if (c < n) store_codes(q, c, n, codes8_any(p.q_dtype, v[i], f));
+        if (c >= n) continue;
+        const uint2 codes = codes8_any(p.q_dtype, v[i], f);
+        with_bool(p.once, [&](auto once) { store_codes<once()>(q, c, n, codes); });
     }
 }
 
@@ -312,7 +321,7 @@ hipError_t launch_norm_x(int res_dtype, const NormParams &p, hipStream_t stream)
 // registers; it stores them once, and grad_weight_kernel adds the parts.
 // Enough workgroups share a CU for one's loads to cover the other's sums: to
 // read the next row ahead as well gains nothing.  8192 x 8192 bf16 with
-// grad_h: 106 + 5 us, 4.9 TB/s, the rate of a large copy.
+// grad_h: 101 + 5 us, 5.1 TB/s, the rate of a large copy.
 
 // D: grad_h's type.
 template <typename G, typename H, typename D, int W, int VPT>
@@ -338,14 +347,16 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64, 4) void norm_grad_rows(NormG
         Raw8<G> gr[VPT];
         Raw8<H> hr[VPT];
         Raw8<D> dr[VPT];
+        with_bool(p.once, [&](auto once) {
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int c = c0 + i * (W * 512);
-            gr[i] = fetch8(static_cast<const G *>(p.g) + row * p.ldg, c, n);
-            hr[i] = fetch8(static_cast<const H *>(p.h) + row * p.ldh, c, n);
-            // (before the first store, since it may be grad_in)
-            if (p.gh) dr[i] = fetch8(static_cast<const D *>(p.gh) + row * p.ldgh, c, n);
-        }
+            for (int i = 0; i < VPT; ++i) {
+                const int c = c0 + i * (W * 512);
+                gr[i] = fetch8<once()>(static_cast<const G *>(p.g) + row * p.ldg, c, n);
+                hr[i] = fetch8<once()>(static_cast<const H *>(p.h) + row * p.ldh, c, n);
+                // (before the first store, since it may be grad_in)
+                if (p.gh) dr[i] = fetch8<once()>(static_cast<const D *>(p.gh) + row * p.ldgh, c, n);
+            }
+        });
         float sq = 0.0f, dot = 0.0f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
@@ -452,22 +463,23 @@ __global__ __launch_bounds__(1024) void norm_grad_long_rows(NormGradParams p, in
     }
 }
 
-// grad_weight: 32 columns a workgroup, 32 half waves that each add every 32nd
-// part, joined in the order of the half waves.
+// grad_weight: 16 columns a workgroup, 64 quarter waves that each add every
+// 64th part, joined in the order of the quarter waves.
 __global__ __launch_bounds__(1024) void grad_weight_kernel(NormGradParams p, int64_t parts)
 {
-    __shared__ float lds[32][33];
-    const int col = threadIdx.x & 31, half = threadIdx.x >> 5;
-    int64_t c = (int64_t)blockIdx.x * 32 + col;
+    __shared__ float lds[64][17];
+    const int col = threadIdx.x & 15, quarter = threadIdx.x >> 4;
+    const int64_t c = (int64_t)blockIdx.x * 16 + col;
     float s = 0.0f;
     if (c < p.n) {
 #pragma unroll 8
-        for (int64_t i = half; i < parts; i += 32) s += p.part[i * p.n + c];
+        for (int64_t i = quarter; i < parts; i += 64) s += p.part[i * p.n + c];
     }
-    lds[half][col] = s;
+    lds[quarter][col] = s;
     __syncthreads();
-    if (half || c >= p.n) return;
-    for (int i = 1; i < 32; ++i) s += lds[i][col];
+    if (quarter || c >= p.n) return;
+#pragma unroll 16
+    for (int i = 1; i < 64; ++i) s += lds[i][col];
     if (p.w_dtype == EMU_DT_BF16)
         static_cast<__bf16 *>(p.gw)[c] = (__bf16)s;
     else if (p.w_dtype == EMU_DT_FP16)
@@ -521,8 +533,12 @@ int64_t norm_grad_parts(int64_t T, int64_t n)
     return most < parts ? most : parts;
 }
 
-hipError_t launch_norm_grad(int g_dtype, int h_dtype, const NormGradParams &p, hipStream_t stream)
+hipError_t launch_norm_grad(int g_dtype, int h_dtype, const NormGradParams &params, hipStream_t stream)
 {
+    NormGradParams p = params;
+    const int64_t size = (g_dtype == EMU_DT_FP32 ? 4 : 2) * (p.gh ? 3 : 2) + (h_dtype == EMU_DT_FP32 ? 4 : 2);
+    // (8192 x 8192 bf16: 100 us past the cache, 110 through it)
+    p.once = p.T * p.n * size > kOnceBytes;
     const int64_t parts = norm_grad_parts(p.T, p.n);
     if (parts > 0) {
         if (g_dtype == EMU_DT_FP32)
@@ -538,12 +554,17 @@ hipError_t launch_norm_grad(int g_dtype, int h_dtype, const NormGradParams &p, h
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL(grad_weight_kernel, dim3((unsigned)((p.n + 31) / 32)), dim3(1024), 0, stream, p, parts);
+    hipLaunchKernelGGL(grad_weight_kernel, dim3((unsigned)((p.n + 15) / 16)), dim3(1024), 0, stream, p, parts);
     return hipGetLastError();
 }
 
-hipError_t launch_norm(int x_dtype, int res_dtype, const NormParams &p, hipStream_t stream)
+hipError_t launch_norm(int x_dtype, int res_dtype, const NormParams &params, hipStream_t stream)
 {
+    NormParams p = params;
+    const int64_t res = !p.res ? 0 : res_dtype == EMU_DT_FP32 ? 4 : 2;
+    // (after x's producer, 8192 x 8192 bf16: 79 us past the cache, 84 through
+    // it; 4096 x 8192: 38 and 44)
+    p.once = p.T * p.n * ((x_dtype == EMU_DT_FP32 ? 4 : 2) + res + (p.h ? res : 0) + 1) > kOnceBytes;
     if (x_dtype == EMU_DT_BF16) return launch_norm_x<__bf16>(res_dtype, p, stream);
     if (x_dtype == EMU_DT_FP16) return launch_norm_x<_Float16>(res_dtype, p, stream);
     return launch_norm_x<float>(res_dtype, p, stream);

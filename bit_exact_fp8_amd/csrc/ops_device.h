@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "../../include/emu_operators.h"
 
 namespace emu {
@@ -31,6 +33,31 @@ __device__ __forceinline__ Raw8<E> load8(const E *p)
 {
     return *reinterpret_cast<const typename Vec8<E>::mem *>(p);
 }
+// ONCE: what is read or written once, and would not fit the last-level cache,
+// passes by it (the launches say from where on, and what it measured).
+template <bool ONCE, typename E>
+__device__ __forceinline__ Raw8<E> load8(const E *p)
+{
+    if constexpr (ONCE) return __builtin_nontemporal_load(reinterpret_cast<const typename Vec8<E>::mem *>(p));
+    return load8(p);
+}
+template <bool ONCE, typename T, typename V>
+__device__ __forceinline__ void store_as(void *p, const V &v)
+{
+    if constexpr (ONCE)
+        __builtin_nontemporal_store(v, reinterpret_cast<T *>(p));
+    else
+        *reinterpret_cast<T *>(p) = v;
+}
+// f(std::true_type) or f(std::false_type)
+template <typename F>
+__device__ __forceinline__ void with_bool(bool b, F f)
+{
+    if (b)
+        f(std::true_type{});
+    else
+        f(std::false_type{});
+}
 template <typename E>
 __device__ __forceinline__ f32x8 widen(const Raw8<E> &v)
 {
@@ -51,10 +78,10 @@ __device__ __forceinline__ f32x8 moved(f32x8 v, int k, float fill = 0.0f)
 // loads are under way before the first is used: fetch8 reads them, or, where
 // the row ends before, its last eight, with the same instruction; settle8
 // then moves those into place, zeros past the end.
-template <typename E>
+template <bool ONCE = false, typename E>
 __device__ __forceinline__ Raw8<E> fetch8(const E *row, int c, int n)
 {
-    if (n >= 8) return load8(row + (c + 8 <= n ? c : n - 8));
+    if (n >= 8) return load8<ONCE>(row + (c + 8 <= n ? c : n - 8));
     Raw8<E> r;
 #pragma unroll
     for (int i = 0; i < 8; ++i) r[i] = c + i < n ? row[c + i] : (E)0.0f;
@@ -105,12 +132,12 @@ __device__ __forceinline__ f32x8 settle8_any(const AnyRaw8 &raw, int dtype, int 
 }
 
 // Elements c .. c + 7, those past n (or all of them) not stored; past the end in pieces of 4, 2 and 1.
-template <typename E>
+template <bool ONCE = false, typename E>
 __device__ __forceinline__ void store8_row(E *row, int c, int n, f32x8 v)
 {
     E *p = row + c;
     if (c + 8 <= n) {
-        *reinterpret_cast<typename Vec8<E>::mem *>(p) = __builtin_convertvector(v, Raw8<E>);
+        store_as<ONCE, typename Vec8<E>::mem>(p, __builtin_convertvector(v, Raw8<E>));
         return;
     }
     const int left = c < n ? n - c : 0;

@@ -8,6 +8,10 @@
 
 namespace emu {
 
+// Bytes read and written beyond which a launch passes by the last-level cache
+// (256 MiB, of which it then finds little that its producer has left there).
+constexpr int64_t kOnceBytes = int64_t(192) << 20;
+
 struct NormParams {
     const void *x, *weight, *res;
     int64_t ldx, ldres;
@@ -20,6 +24,7 @@ struct NormParams {
     float *row_scales;
     void *h;              // null, or of the residual's type
     int64_t ldh;
+    bool once;            // nothing of this size stays in a cache
 };
 // x_dtype: EMU_DT_BF16 .. FP32; res_dtype likewise (x's or FP32), ignored without a residual.
 hipError_t launch_norm(int x_dtype, int res_dtype, const NormParams &p, hipStream_t stream);
@@ -34,6 +39,7 @@ struct NormGradParams {
     int64_t ldgi;
     void *gw;
     float *part;          // [norm_grad_parts(T, n), n]
+    bool once;            // nothing of this size stays in a cache
 };
 int64_t norm_grad_parts(int64_t T, int64_t n);
 hipError_t launch_norm_grad(int g_dtype, int h_dtype, const NormGradParams &p, hipStream_t stream);
