@@ -25,6 +25,7 @@ constexpr int kThreads = 256;
 constexpr int kTile = kThreads * 8;          // logits that a workgroup reads at once
 constexpr float kLowest = -3.402823466e+38f;
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
+constexpr float kLog2eRest = (float)(1.44269504088896341 - (double)kLog2e);
 // e^-104 < 2^-150 rounds to 0 in binary32: differences are cut there, which
 // keeps e^d d at 0 for a logit of -inf.
 constexpr float kFar = -104.0f;
@@ -643,7 +644,12 @@ __global__ __launch_bounds__(kThreads) void logp_grad_rows(LogpGradParams p, int
     const bool empty = lse == -INFINITY;
     const auto value = [&](float x) {
         const float d = fmaxf(x - lse, kFar);
-        return exp_of(d) * __builtin_fmaf(-ge, d, A);
+        float e = exp_of(d);
+        if (sizeof(Z) == 4) {  // what d log2(e) was rounded by, up to 2^-24 |d| of the result
+            const float rest = __builtin_fmaf(d, kLog2eRest, __builtin_fmaf(d, kLog2e, -(d * kLog2e)));
+            e = __builtin_fmaf(e, rest * kLn2, e);
+        }
+        return e * __builtin_fmaf(-ge, d, A);
     };
     if (H) __syncthreads();
     for (int64_t c = s0 + threadIdx.x * 8; c < s1; c += kTile) {

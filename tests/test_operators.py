@@ -823,3 +823,58 @@ def test_leading_axes_and_argument_types(dev):
     with pytest.raises(fw.EmuError) as e:
         fw.add_rms_norm_quant(base, w, out_dtype="int8")
     assert e.value.status == 3
+
+
+# ---- all of them together ---------------------------------------------------
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["int8", "fp8"])
+@pytest.mark.parametrize("T,n,V", [(1, 64, 96), (33, 192, 500)])
+def test_policy_step(dev, kind, T, n, V):
+    """A step's loss and gradients against autograd in 64 bits, from the step's own codes."""
+    from bit_exact_fp8_amd import policy_step as ps
+    note(f"policy step {kind} T={T} n={n} V={V}")
+    gen = rng(T + n)
+    V -= V % 16
+    weight = rand(gen, V, n, std=n ** -0.5)
+    branch, stream, nw = rand(gen, T, n), rand(gen, T, n), 1 + rand(gen, n, std=0.1)
+    tokens, adv = torch.randint(0, V, (T,), generator=gen), rand(gen, T)
+    other = rand(gen, T, n, std=1e-3)
+    head = ps.int8_head(weight.to(dev)) if kind == "int8" else ps.fp8_head(weight.to(dev), 1 / 32)
+    s = ps.policy_step(branch.to(dev), stream.to(dev), nw.to(dev), head, tokens.to(dev), adv.to(dev), 0.05,
+                       grad_stream=other.to(dev))
+    codes, scale, _ = fw.add_rms_norm_quant(branch.to(dev), nw.to(dev), stream.to(dev), out_dtype=I8 if kind == "int8" else E4,
+                                            scale=head.in_scale)
+    W = head.weight().cpu().to(f64)
+    if kind == "int8":
+        z = (codes.float() * scale).cpu().to(f64) @ W.t()
+    else:  # (the emulated product's own values: it cuts its sums)
+        z = fw.scaled_mm(codes, head.codes.t(), scale, head.scale, out_dtype=SF, use_fast_accum=True).cpu().to(f64)
+    z.requires_grad_()
+    lp = torch.log_softmax(z, 1)
+    ent = -(lp.exp() * lp).sum(1)
+    loss = -(adv.to(f64) * lp.gather(1, tokens[:, None])[:, 0] + 0.05 * ent).mean()
+    loss.backward()
+    h = (branch.to(f64) + stream.to(f64)).requires_grad_()
+    w = nw.to(f64).requires_grad_()
+    y = h / (h.pow(2).mean(1, keepdim=True) + 1e-6).sqrt() * w
+    dy = z.grad @ W
+    y.backward(dy)
+    # logits of some 4 with errors of F (1 + |z|); p and its gradient follow
+    # them, and the sums over V and n add their terms' absolute values
+    zmax = 1 + z.detach().abs().amax()
+    dz = F * 4 * zmax * (z.grad.abs() + adv.to(f64).abs().max() / T * lp.detach().exp())
+    ddy = dz @ W.abs() + F * (z.grad.abs() @ W.abs())
+    r = (h.detach().pow(2).mean(1, keepdim=True) + 1e-6).rsqrt()
+    u, nv = dy.abs() * w.detach().abs(), h.detach().abs() * r
+    du = ddy * w.detach().abs() + F * u
+    dh = r * (du + nv * (du * nv).mean(1, keepdim=True) + F * nv * (u * nv).mean(1, keepdim=True))
+    close(s.loss[None], loss.detach()[None], (F * 4 * zmax * (1 + adv.to(f64).abs().mean()) * 10)[None], "loss")
+    close(s.grad_stream, h.grad + other.to(f64), dh + F * (h.grad.abs() + other.to(f64).abs()), "stream's gradient")
+    close(s.grad_weight, w.grad, (ddy * nv + F * dy.abs() * nv).sum(0), "weight's gradient")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["int8", "fp8"])
+def test_policy_step_learns(dev, kind):
+    from bit_exact_fp8_amd import policy_step as ps
+    assert ps.main(["--head", kind, "--steps", "1"]) > 2 * ps.main(["--head", kind, "--steps", "12"])
