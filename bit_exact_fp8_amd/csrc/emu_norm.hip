@@ -323,17 +323,15 @@ hipError_t launch_norm_x(int res_dtype, const NormParams &p, hipStream_t stream)
 // read the next row ahead as well gains nothing.  8192 x 8192 bf16 with
 // grad_h: 101 + 5 us, 5.1 TB/s, the rate of a large copy.
 
-// D: grad_h's type.
-template <typename G, typename H, typename D, int W, int VPT>
-__global__ __launch_bounds__(W == 1 ? 256 : W * 64, 4) void norm_grad_rows(NormGradParams p, int64_t parts)
+// D: grad_h's type.  W waves hold a row, as in norm_rows; a workgroup has ROWS
+// rows at a time, and the sums of all of them go into its one part.
+template <typename G, typename H, typename D, int W, int VPT, int ROWS>
+__global__ __launch_bounds__(W * ROWS * 64, 4) void norm_grad_rows(NormGradParams p, int64_t parts)
 {
-    constexpr int kRows = W == 1 ? 4 : 1;  // rows at a time in a workgroup
-    __shared__ float2 lds[2][W];
-    __shared__ float share[W == 1 ? 3 * VPT * 512 : 1];
-    const int lane = threadIdx.x & 63, wv = wave_index();
-    const int wave = W == 1 ? 0 : wv;
+    __shared__ float2 lds[2][ROWS][W];
+    __shared__ float share[ROWS > 1 ? (ROWS - 1) * W * VPT * 512 : 1];
+    const int lane = threadIdx.x & 63, wave = wave_index() % W, group = wave_index() / W;
     const int n = (int)p.n;
-    const int64_t step = parts * kRows;
     __builtin_assume(n >= 8);
     const int c0 = (wave * 64 + lane) * 8;
 
@@ -341,8 +339,11 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64, 4) void norm_grad_rows(NormG
 #pragma unroll
     for (int i = 0; i < VPT; ++i) gw[i] = 0.0f;
     const auto weight = [&](int c) { return settle8_any(fetch8_any(p.weight, p.w_dtype, c, n), p.w_dtype, c, n); };
-    int64_t row = (int64_t)blockIdx.x * kRows + (W == 1 ? wv : 0);
-    for (int turn = 0; row < p.T; row += step, turn ^= 1) {
+    int turn = 0;
+    for (int64_t first = (int64_t)blockIdx.x * ROWS; first < p.T; first += parts * ROWS, turn ^= 1) {
+        // (a group past the last row goes along to the barriers)
+        const bool mine = first + group < p.T;
+        const int64_t row = mine ? first + group : p.T - 1;
         f32x8 gv[VPT], hv[VPT];
         Raw8<G> gr[VPT];
         Raw8<H> hr[VPT];
@@ -373,15 +374,16 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64, 4) void norm_grad_rows(NormG
         sq = wave_sum(sq);
         dot = wave_sum(dot);
         if (W > 1) {
-            if (lane == 0) lds[turn][wave] = make_float2(sq, dot);
+            if (lane == 0) lds[turn][group][wave] = make_float2(sq, dot);
             __syncthreads();  // two arrays in turn: a wave is at most one barrier ahead
             sq = dot = 0.0f;
 #pragma unroll
             for (int i = 0; i < W; ++i) {
-                sq += lds[turn][i].x;
-                dot += lds[turn][i].y;
+                sq += lds[turn][group][i].x;
+                dot += lds[turn][group][i].y;
             }
         }
+        if (ROWS > 1 && !mine) continue;
         const float r = 1.0f / sqrtf(sq / (float)n + p.eps);
         const float mean = dot * r / (float)n;
         G *gi = static_cast<G *>(p.gi) + row * p.ldgi;
@@ -395,20 +397,21 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64, 4) void norm_grad_rows(NormG
             store8_row(gi, c, n, d);
         }
     }
-    if (W == 1) {  // the four waves' sums, in the order of the waves
-        if (wv) {
+    if (ROWS > 1) {  // the groups' sums, in their order
+        float *at = share + wave * VPT * 512 + lane;
+        if (group) {
 #pragma unroll
             for (int i = 0; i < VPT; ++i)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) share[(wv - 1) * VPT * 512 + (i * 8 + j) * 64 + lane] = gw[i][j];
+                for (int j = 0; j < 8; ++j) at[(group - 1) * W * VPT * 512 + (i * 8 + j) * 64] = gw[i][j];
         }
         __syncthreads();
-        if (wv) return;
-        for (int o = 0; o < 3; ++o)
+        if (group) return;
+        for (int o = 0; o < ROWS - 1; ++o)
 #pragma unroll
             for (int i = 0; i < VPT; ++i)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) gw[i][j] += share[o * VPT * 512 + (i * 8 + j) * 64 + lane];
+                for (int j = 0; j < 8; ++j) gw[i][j] += at[o * W * VPT * 512 + (i * 8 + j) * 64];
     }
     float *part = p.part + (int64_t)blockIdx.x * n;
 #pragma unroll
@@ -488,25 +491,33 @@ __global__ __launch_bounds__(1024) void grad_weight_kernel(NormGradParams p, int
         static_cast<float *>(p.gw)[c] = s;
 }
 
+// Rows at a time in a workgroup.
+int64_t grad_rows_at_once(int64_t n) { return n < 8 ? 1 : n <= 1024 ? 4 : n <= 4096 ? 2 : 1; }
+
+template <typename G, typename H, typename D, int W, int VPT, int ROWS>
+void launch_grad_rows(const NormGradParams &p, int64_t parts, hipStream_t stream)
+{
+    hipLaunchKernelGGL((norm_grad_rows<G, H, D, W, VPT, ROWS>), dim3((unsigned)parts), dim3(W * ROWS * 64), 0, stream, p, parts);
+}
+
 template <typename G, typename H, typename D>
 void launch_norm_grad_of(const NormGradParams &p, int64_t parts, hipStream_t stream)
 {
     const int64_t n = p.n;
-    const dim3 grid((unsigned)parts);
     if (n < 8 || n > 16384)
-        hipLaunchKernelGGL((norm_grad_long_rows<G, H>), grid, dim3(1024), 0, stream, p, parts);
+        hipLaunchKernelGGL((norm_grad_long_rows<G, H>), dim3((unsigned)parts), dim3(1024), 0, stream, p, parts);
     else if (n <= 512)
-        hipLaunchKernelGGL((norm_grad_rows<G, H, D, 1, 1>), grid, dim3(256), 0, stream, p, parts);
+        launch_grad_rows<G, H, D, 1, 1, 4>(p, parts, stream);
     else if (n <= 1024)
-        hipLaunchKernelGGL((norm_grad_rows<G, H, D, 1, 2>), grid, dim3(256), 0, stream, p, parts);
+        launch_grad_rows<G, H, D, 1, 2, 4>(p, parts, stream);
     else if (n <= 2048)
-        hipLaunchKernelGGL((norm_grad_rows<G, H, D, 4, 1>), grid, dim3(256), 0, stream, p, parts);
+        launch_grad_rows<G, H, D, 4, 1, 2>(p, parts, stream);
     else if (n <= 4096)
-        hipLaunchKernelGGL((norm_grad_rows<G, H, D, 8, 1>), grid, dim3(512), 0, stream, p, parts);
+        launch_grad_rows<G, H, D, 8, 1, 2>(p, parts, stream);
     else if (n <= 8192)
-        hipLaunchKernelGGL((norm_grad_rows<G, H, D, 8, 2>), grid, dim3(512), 0, stream, p, parts);
+        launch_grad_rows<G, H, D, 8, 2, 1>(p, parts, stream);
     else
-        hipLaunchKernelGGL((norm_grad_rows<G, H, D, 16, 2>), grid, dim3(1024), 0, stream, p, parts);
+        launch_grad_rows<G, H, D, 16, 2, 1>(p, parts, stream);
 }
 
 template <typename G, typename H>
@@ -521,14 +532,12 @@ void launch_norm_grad_gh(const NormGradParams &p, int64_t parts, hipStream_t str
 }  // namespace
 
 // Workgroups of the gradient, each with a part of grad_weight in the
-// workspace: 16 waves for each CU, but over 512 only where each gets 8 rows
-// (8192 x 2048: 25 us with 1024 parts, 30 with 512; 1023 x 1925, both kernels:
-// 17 and 13 us), and one for each row (or four rows of up to 1,024 values, a
-// row to a wave).
+// workspace: 16 waves for each CU (rows of up to 1,024 values take four for
+// that, which is done only where each workgroup gets 8 turns), and no more than have rows.
 int64_t norm_grad_parts(int64_t T, int64_t n)
 {
-    const int64_t most = n >= 8 && n <= 1024 ? (T + 3) / 4 : T;
-    int64_t parts = n <= 2048 ? 1024 : n <= 8192 ? 512 : 256;
+    const int64_t at_once = grad_rows_at_once(n), most = (T + at_once - 1) / at_once;
+    int64_t parts = n <= 1024 ? 1024 : n <= 2048 ? 512 : n <= 4096 ? 256 : n <= 8192 ? 512 : 256;
     if (parts > 512 && parts > T / 8) parts = T / 8 > 512 ? T / 8 : 512;
     return most < parts ? most : parts;
 }
