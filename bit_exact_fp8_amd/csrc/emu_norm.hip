@@ -323,6 +323,9 @@ hipError_t launch_norm_x(int res_dtype, const NormParams &p, hipStream_t stream)
 // read the next row ahead as well gains nothing.  8192 x 8192 bf16 with
 // grad_h: 101 + 5 us, 5.1 TB/s, the rate of a large copy.
 
+// A part's place in the workspace, whole cache lines (1023 x 1925: 8.0 us, 9.0 without).
+__host__ __device__ constexpr int64_t part_ld(int64_t n) { return (n + 31) / 32 * 32; }
+
 // D: grad_h's type.  W waves hold a row, as in norm_rows; a workgroup has ROWS
 // rows at a time, and the sums of all of them go into its one part.
 template <typename G, typename H, typename D, int W, int VPT, int ROWS>
@@ -413,7 +416,7 @@ __global__ __launch_bounds__(W * ROWS * 64, 4) void norm_grad_rows(NormGradParam
 #pragma unroll
                 for (int j = 0; j < 8; ++j) gw[i][j] += at[o * W * VPT * 512 + (i * 8 + j) * 64];
     }
-    float *part = p.part + (int64_t)blockIdx.x * n;
+    float *part = p.part + blockIdx.x * part_ld(n);
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
         store8_row(part, c0 + i * (W * 512), n, gw[i]);
@@ -428,7 +431,7 @@ __global__ __launch_bounds__(1024) void norm_grad_long_rows(NormGradParams p, in
     __shared__ float lds[2][2][16];
     const int lane = threadIdx.x & 63, wave = wave_index();
     const int n = (int)p.n;
-    float *part = p.part + (int64_t)blockIdx.x * n;
+    float *part = p.part + blockIdx.x * part_ld(n);
     const auto weight = [&](int c) { return settle8_any(fetch8_any(p.weight, p.w_dtype, c, n), p.w_dtype, c, n); };
     int turn = 0;
     bool first = true;
@@ -476,7 +479,7 @@ __global__ __launch_bounds__(1024) void grad_weight_kernel(NormGradParams p, int
     float s = 0.0f;
     if (c < p.n) {
 #pragma unroll 8
-        for (int64_t i = quarter; i < parts; i += 64) s += p.part[i * p.n + c];
+        for (int64_t i = quarter; i < parts; i += 64) s += p.part[i * part_ld(p.n) + c];
     }
     lds[quarter][col] = s;
     __syncthreads();
@@ -534,6 +537,8 @@ void launch_norm_grad_gh(const NormGradParams &p, int64_t parts, hipStream_t str
 // Workgroups of the gradient, each with a part of grad_weight in the
 // workspace: 16 waves for each CU (rows of up to 1,024 values take four for
 // that, which is done only where each workgroup gets 8 turns), and no more than have rows.
+int64_t norm_grad_part_ld(int64_t n) { return part_ld(n); }
+
 int64_t norm_grad_parts(int64_t T, int64_t n)
 {
     const int64_t at_once = grad_rows_at_once(n), most = (T + at_once - 1) / at_once;

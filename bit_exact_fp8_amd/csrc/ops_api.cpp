@@ -88,7 +88,7 @@ emu_status emu_add_rms_norm_quant(const void *x, emu_dtype x_dtype, int64_t ldx,
 size_t emu_add_rms_norm_backward_workspace(int64_t T, int64_t n)
 {
     if (T < 0 || n < 0 || T > kMaxRows || n > kMaxCols) return 0;
-    return (size_t)(emu::norm_grad_parts(T, n) * n) * 4;
+    return (size_t)(emu::norm_grad_parts(T, n) * emu::norm_grad_part_ld(n)) * 4;
 }
 
 emu_status emu_add_rms_norm_backward(const void *g, emu_dtype g_dtype, int64_t ldg, const void *h, emu_dtype h_dtype,

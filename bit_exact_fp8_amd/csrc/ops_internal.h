@@ -38,10 +38,11 @@ struct NormGradParams {
     void *gi;
     int64_t ldgi;
     void *gw;
-    float *part;          // [norm_grad_parts(T, n), n]
+    float *part;          // [norm_grad_parts(T, n), norm_grad_part_ld(n)]
     bool once;            // nothing of this size stays in a cache
 };
 int64_t norm_grad_parts(int64_t T, int64_t n);
+int64_t norm_grad_part_ld(int64_t n);
 hipError_t launch_norm_grad(int g_dtype, int h_dtype, const NormGradParams &p, hipStream_t stream);
 
 struct Int8Params {
