@@ -6,7 +6,8 @@ chains from incoming accumulators), compiled in parallel and linked with the
 dispatcher, the combine kernel, the deferred-infinity kernels
 (emu_specials.hip), the no-allocation entry point (emu_noalloc.hip), the C
 ABI and the operators beside the product (emu_norm.hip, emu_int8.hip,
-emu_logprobs.hip, ops_api.cpp)."""
+emu_logprobs.hip, ops_api.cpp).  The operators' Python calls (ops_binding.cpp)
+are a module of their own, _ops.so."""
 from __future__ import annotations
 
 import os

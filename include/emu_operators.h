@@ -54,6 +54,8 @@ typedef enum {
  * residual's type that takes v; it may be the residual itself.
  * A NaN in a row's y gives that row the scale NaN (scale == NULL) and NaN
  * codes, 0 for int8, which has none; an infinity in v makes y NaN.
+ * The squares of v are summed in binary32, in which values beyond 1.8e19
+ * overflow: such a row counts as one with an infinite mean (r = 0).
  * n = 0 with T > 0 is refused; T = 0 does nothing.
  */
 EMU_API emu_status emu_add_rms_norm_quant(const void *x, emu_dtype x_dtype, int64_t ldx,
@@ -73,8 +75,9 @@ EMU_API emu_status emu_add_rms_norm_quant(const void *x, emu_dtype x_dtype, int6
  * grad_in [T, n] of g's type is the gradient of x and of the residual alike.
  * h is of g's type or fp32, weight of g's type or fp32, grad_h NULL or of
  * g's type or fp32; grad_in may be g or (of its type) grad_h itself.
- * grad_weight [n] of weight's type; T = 0 writes zeros to it.  workspace: emu_add_rms_norm_backward_workspace(T, n)
- * bytes, 16-byte aligned, contents on entry and return do not matter.
+ * grad_weight [n] of weight's type; T = 0 writes zeros to it.  workspace:
+ * emu_add_rms_norm_backward_workspace(T, n) bytes, 16-byte aligned, contents
+ * on entry and return do not matter.
  */
 EMU_API emu_status emu_add_rms_norm_backward(const void *g, emu_dtype g_dtype, int64_t ldg,
                                              const void *h, emu_dtype h_dtype, int64_t ldh,
