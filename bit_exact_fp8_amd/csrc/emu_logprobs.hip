@@ -677,7 +677,10 @@ __global__ __launch_bounds__(kThreads) void logp_grad_rows(LogpGradParams p, int
 template <typename Z>
 hipError_t launch_logp_grad_of(const LogpGradParams &p, hipStream_t stream)
 {
-    const int64_t span = 4 * kTile;
+    // four tiles to a workgroup, fewer where there would not be 8 workgroups for
+    // each CU (2 x 38336: 4.0 us with one, 5.4 with four)
+    int64_t span = 4 * kTile;
+    while (span > kTile && p.T * ((p.V + span - 1) / span) < 2048) span /= 2;
     const int64_t P = (p.V + span - 1) / span;
     const size_t lds = (size_t)(p.C + p.k) * 12;
     // (as in launch_logp_of: 4096 x 65536 bf16 163 us past the cache and 187
