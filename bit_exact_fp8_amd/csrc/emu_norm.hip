@@ -3,7 +3,8 @@
 // Forward: v = x + residual, y = v r w with r = 1 / sqrt(mean(v^2) + eps),
 // codes of y / scale.  Each value is needed three times (for the mean, for
 // the row's largest |y|, for its code), so a row is held in registers and
-// read once.  16384 x 8192 bf16: 155 us, 6.0 TB/s.
+// read once; the weight is read again for the codes, since to hold the products'
+// rests instead takes a workgroup off each CU (16384 x 8192: 176 us, 163 now, 5.8 TB/s).
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -16,11 +17,12 @@ namespace emu {
 namespace {
 
 // A row's way from v to codes: u = v 2^e w with 2^e near r (the power of two
-// changes no digit and keeps v w from overflowing), then u f with
-// f = r 2^-e / scale, made in 64 bits and kept as the sum of two binary32
-// values.  A code is so off by two roundings, not by the five of v r, times
-// w, over scale with an r of 32 bits: next to a border fewer codes fall to
-// the other side, and no division is left.  A scale under 2^-100, whose f may
+// changes no digit and keeps v w from overflowing), held with what its
+// rounding cut off, then u f with f = r 2^-e / scale, made in 64 bits and kept
+// as the sum of two binary32 values.  Where the product lies on a border it is
+// rounded to odd, so that the code's rounding after it is that of the whole
+// value and no code falls to the other side (rounded to nearest, some one in
+// 2 million does; this costs 2%), and no division is left.  A scale under 2^-100, whose f may
 // overflow, divides.
 struct Factor {
     float power, hi, lo;  // 2^e; f
@@ -51,14 +53,40 @@ __device__ __forceinline__ float cut(float v)
     return v > most ? most : v < -most ? -most : v;
 }
 
-// 8 codes, rounded to nearest even.
+// u f rounded to odd: to the neighbour with an odd last digit where it is not exact.
+__device__ __forceinline__ float product_to_odd(float u, float rest, const Factor &f)
+{
+    // (an infinite u has no rest)
+    const float t = __builtin_fabsf(u) < INFINITY ? __builtin_fmaf(u, f.lo, rest * f.hi) : 0.0f;
+    const float y = __builtin_fmaf(u, f.hi, t);
+    const float off = __builtin_fmaf(u, f.hi, -y) + t;  // the value less y
+    const uint32_t bits = __float_as_uint(y);
+    const uint32_t toward = bits - ((__float_as_uint(off) ^ bits) >> 31);  // the value lies beyond it, away from 0
+    const bool plain = __builtin_fabsf(y) > 1e-30f && __builtin_fabsf(y) < INFINITY;  // (below, the code is 0 anyway)
+    return off != 0.0f && plain ? __uint_as_float(toward | 1) : y;
+}
+
+// 8 codes of u + rest, rounded to nearest even.
 template <int Q>
-__device__ __forceinline__ uint2 codes8(const f32x8 &u, const Factor &f)
+__device__ __forceinline__ uint2 codes8(const f32x8 &u, const f32x8 &rest, const Factor &f)
 {
     f32x8 y;
     if (f.scale >= 7.888609052e-31f) {
+        // A product to nearest has its code on the wrong side only if it lies
+        // on a border, whose last 19 (int8: 16) bits are 0: where any does
+        // (an infinity and a NaN of it too), all are made again.  To round
+        // every one to odd costs 16384 x 8192 10%.
+        uint32_t least = ~0u;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = __builtin_fmaf(u[i], f.hi, u[i] * f.lo);
+        for (int i = 0; i < 8; ++i) {
+            y[i] = __builtin_fmaf(u[i], f.hi, __builtin_fmaf(u[i], f.lo, rest[i] * f.hi));
+            const uint32_t last = __float_as_uint(y[i]) & (Q == EMU_DT_INT8 ? 0xFFFFu : 0x7FFFFu);
+            least = last < least ? last : least;
+        }
+        if (__any(least == 0)) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = product_to_odd(u[i], rest[i], f);
+        }
     } else {
         y = u * f.rest / f.scale;
     }
@@ -118,11 +146,19 @@ __device__ __forceinline__ void store_codes(uint8_t *row, int c, int n, const ui
     if (left & 1) *p = (uint8_t)v;
 }
 
-__device__ __forceinline__ uint2 codes8_any(int q_dtype, const f32x8 &u, const Factor &f)
+__device__ __forceinline__ uint2 codes8_any(int q_dtype, const f32x8 &u, const f32x8 &rest, const Factor &f)
 {
-    if (q_dtype == EMU_DT_INT8) return codes8<EMU_DT_INT8>(u, f);
-    if (q_dtype == EMU_DT_E4M3FN) return codes8<EMU_DT_E4M3FN>(u, f);
-    return codes8<EMU_DT_E5M2>(u, f);
+    if (q_dtype == EMU_DT_INT8) return codes8<EMU_DT_INT8>(u, rest, f);
+    if (q_dtype == EMU_DT_E4M3FN) return codes8<EMU_DT_E4M3FN>(u, rest, f);
+    return codes8<EMU_DT_E5M2>(u, rest, f);
+}
+// u and rest of 8 values
+__device__ __forceinline__ f32x8 scaled(const f32x8 &v, const f32x8 &w, const Factor &f, f32x8 &rest)
+{
+    const f32x8 x = v * f.power, u = x * w;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) rest[i] = __builtin_fmaf(x[i], w[i], -u[i]);
+    return u;
 }
 
 __device__ __forceinline__ float most_of(int q_dtype)
@@ -192,20 +228,18 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_rows(NormParams p)
         }
     }
     Factor f = factor_of(r);
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int c = c0 + i * (W * 512);
-        v[i] = v[i] * f.power * settle8_any(fetch8_any(p.weight, p.w_dtype, c, n), p.w_dtype, c, n);
-    }
+    const auto weight = [&](int c) { return settle8_any(fetch8_any(p.weight, p.w_dtype, c, n), p.w_dtype, c, n); };
     float scale;
     if (p.scale) {
         scale = *p.scale;
     } else {
         float a = 0.0f;
 #pragma unroll
-        for (int i = 0; i < VPT; ++i)
+        for (int i = 0; i < VPT; ++i) {
+            const f32x8 u = v[i] * f.power * weight(c0 + i * (W * 512));
 #pragma unroll
-            for (int j = 0; j < 8; ++j) a = __builtin_elementwise_maximum(a, __builtin_fabsf(v[i][j]));
+            for (int j = 0; j < 8; ++j) a = __builtin_elementwise_maximum(a, __builtin_fabsf(u[j]));
+        }
         scale = own_scale(row_max<W>(a, maxima, wave, lane), f, p.q_dtype);
         if (wave == 0 && lane == 0) p.row_scales[row] = scale;
     }
@@ -215,7 +249,9 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_rows(NormParams p)
     for (int i = 0; i < VPT; ++i) {
         const int c = c0 + i * (W * 512);
         if (c >= n) continue;
-        const uint2 codes = codes8_any(p.q_dtype, v[i], f);
+        f32x8 rest;
+        const f32x8 u = scaled(v[i], weight(c), f, rest);
+        const uint2 codes = codes8_any(p.q_dtype, u, rest, f);
         with_bool(p.once, [&](auto once) { store_codes<once()>(q, c, n, codes); });
     }
 }
@@ -274,7 +310,9 @@ __global__ __launch_bounds__(1024) void norm_long_rows(NormParams p)
         if constexpr (kRes) {
             if (p.h) store8_row(static_cast<R *>(p.h) + row * p.ldh, c, n, v);
         }
-        store_codes(q, c, n, codes8_any(p.q_dtype, v * f.power * weight(c), f));
+        f32x8 rest;
+        const f32x8 u = scaled(v, weight(c), f, rest);
+        store_codes(q, c, n, codes8_any(p.q_dtype, u, rest, f));
     }
 }
 

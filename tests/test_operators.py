@@ -878,3 +878,39 @@ def test_policy_step(dev, kind, T, n, V):
 def test_policy_step_learns(dev, kind):
     from bit_exact_fp8_amd import policy_step as ps
     assert ps.main(["--head", kind, "--steps", "1"]) > 2 * ps.main(["--head", kind, "--steps", "12"])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("out", [E4, E5, I8])
+@pytest.mark.parametrize("n", [512, 1920, 8192, 20000])
+def test_norm_codes_are_the_nearest(dev, out, n):
+    """Codes of values that lie at and next to the borders between two: with
+    ones and minus ones r is known, and a weight of a border's value (and its
+    neighbours in binary32) puts y there.  The oracle is exact but for r's 2^-50."""
+    q, r = MOST[out], 1 / math.sqrt(1 + 0.25)
+    v = torch.ones(4, n)
+    v[:, ::3] = -1
+    grid = torch.arange(1, 127, dtype=f64) + 0.5 if out == I8 else None
+    if grid is None:
+        codes = torch.arange(1, 256, dtype=torch.uint8).view(out).to(f64)
+        codes = codes[codes.isfinite() & (codes > 2.0 ** -9)].sort().values
+        grid = (codes[1:] + codes[:-1]) / 2
+    border = grid[torch.arange(n) % len(grid)]
+    w = (border / r).to(SF)
+    step = torch.tensor([-2, -1, 0, 1, 2])[(torch.arange(n) // len(grid)) % 5].to(torch.int32)
+    w = (w.view(torch.int32) + step).view(SF)
+    one = torch.ones(1)
+    note(f"norm codes {out} n={n}")
+    codes, _, _ = fw.add_rms_norm_quant(v.to(dev), w.to(dev), eps=0.25, out_dtype=out, scale=one.to(dev))
+    y = (v.to(f64) * r * w.to(f64)).clamp(-q, q)
+    got = codes.cpu().to(f64)
+    # none of the type's values is nearer than the code
+    if out == I8:
+        near = (y - y.round()).abs()
+    else:
+        values = torch.arange(0, 256, dtype=torch.uint8).view(out).to(f64)
+        values = values[values.isfinite()].sort().values.unique()
+        at = torch.searchsorted(values, y.contiguous()).clamp(1, len(values) - 1)
+        near = torch.minimum((values[at] - y).abs(), (values[at - 1] - y).abs())
+    off = (got - y).abs() - near
+    assert float((off / y.abs()).max()) <= 2.0 ** -46, float((off / y.abs()).max())
