@@ -41,13 +41,16 @@ __device__ __forceinline__ Raw8<E> load8(const E *p)
     if constexpr (ONCE) return __builtin_nontemporal_load(reinterpret_cast<const typename Vec8<E>::mem *>(p));
     return load8(p);
 }
-template <bool ONCE, typename T, typename V>
-__device__ __forceinline__ void store_as(void *p, const V &v)
+// (the vector's lower alignment belongs to its typedef and is lost where that
+// is a template's argument, so the pointer is made here)
+template <bool ONCE, typename E>
+__device__ __forceinline__ void store8(E *p, const Raw8<E> &v)
 {
+    typedef typename Vec8<E>::mem mem;
     if constexpr (ONCE)
-        __builtin_nontemporal_store(v, reinterpret_cast<T *>(p));
+        __builtin_nontemporal_store(v, reinterpret_cast<mem *>(p));
     else
-        *reinterpret_cast<T *>(p) = v;
+        *reinterpret_cast<mem *>(p) = v;
 }
 // f(std::true_type) or f(std::false_type)
 template <typename F>
@@ -137,7 +140,7 @@ __device__ __forceinline__ void store8_row(E *row, int c, int n, f32x8 v)
 {
     E *p = row + c;
     if (c + 8 <= n) {
-        store_as<ONCE, typename Vec8<E>::mem>(p, __builtin_convertvector(v, Raw8<E>));
+        store8<ONCE>(p, __builtin_convertvector(v, Raw8<E>));
         return;
     }
     const int left = c < n ? n - c : 0;
