@@ -24,7 +24,10 @@ namespace {
 // value and no code falls to the other side (rounded to nearest, some one in
 // 2 million does; this costs 2%), and no division is left.  A scale under 2^-100, whose f may
 // overflow, divides.
+// Where r is 0 (the squares of the row overflowed) the power is 0 and the rest
+// 1: finite values become 0 whatever their weights, an infinity NaN.
 struct Factor {
+    double whole;         // r 2^-e
     float power, hi, lo;  // 2^e; f
     float rest, scale;    // r 2^-e
 };
@@ -32,14 +35,15 @@ __device__ __forceinline__ Factor factor_of(double r)
 {
     Factor f;
     const int e = r > 0.0 && r < 1e300 ? __builtin_amdgcn_frexp_exp(r) : 0;
-    f.power = __builtin_amdgcn_ldexpf(1.0f, e);
-    f.rest = (float)(r / (double)f.power);
+    f.power = r == 0.0 ? 0.0f : __builtin_amdgcn_ldexpf(1.0f, e);
+    f.whole = r == 0.0 ? 1.0 : __builtin_amdgcn_ldexp(r, -e);
+    f.rest = (float)f.whole;
     f.hi = f.lo = f.scale = 0.0f;
     return f;
 }
-__device__ __forceinline__ void set_scale(Factor &f, double r, float scale)
+__device__ __forceinline__ void set_scale(Factor &f, float scale)
 {
-    const double q = r / (double)f.power / (double)scale;
+    const double q = f.whole / (double)scale;
     f.hi = (float)q;
     f.lo = (float)(q - (double)f.hi);
     f.scale = scale;
@@ -243,7 +247,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_rows(NormParams p)
         scale = own_scale(row_max<W>(a, maxima, wave, lane), f, p.q_dtype);
         if (wave == 0 && lane == 0) p.row_scales[row] = scale;
     }
-    set_scale(f, r, scale);
+    set_scale(f, scale);
     uint8_t *q = static_cast<uint8_t *>(p.q) + row * p.ldq;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
@@ -303,7 +307,7 @@ __global__ __launch_bounds__(1024) void norm_long_rows(NormParams p)
         scale = own_scale(row_max<16>(a, maxima, wave, lane), f, p.q_dtype);
         if (threadIdx.x == 0) p.row_scales[row] = scale;
     }
-    set_scale(f, r, scale);
+    set_scale(f, scale);
     uint8_t *q = static_cast<uint8_t *>(p.q) + row * p.ldq;
     for (int c = threadIdx.x * 8; c < n; c += 8192) {
         const f32x8 v = value(c);

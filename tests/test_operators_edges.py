@@ -1,12 +1,15 @@
 """What tests/test_operators.py leaves of include/emu_operators.h: the
 alignment that the kernels' memory accesses claim, refusals of what autograd
 would lose, and the paths that only large or unusual calls take."""
+import math
 import os
 import re
 import subprocess
 
 import pytest
+import torch
 
+import bit_exact_fp8_amd as fw
 from bit_exact_fp8_amd import build
 
 ELEMENT = {"float": 4, "half": 2, "bfloat": 2}
@@ -30,3 +33,31 @@ def test_rows_are_accessed_with_their_elements_alignment(source, tmp_path):
             wrong.append(line.strip())
     assert min(seen.values()) > 0
     assert not wrong, (len(wrong), wrong[:3])
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    return torch.device("cuda:0")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("out", [torch.float8_e4m3fn, torch.float8_e5m2, torch.int8])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n", [40, 2000, 20000])
+def test_norm_rows_whose_squares_overflow(dev, n, dtype, out):
+    """Finite values beyond 1.8e19 have an infinite mean and y = 0, also where
+    a value times its weight is beyond binary32; an infinity stays NaN."""
+    x = torch.full((3, n), 3e38, device=dev).to(dtype)
+    x[1, ::2] = -1e30
+    x[2, n // 2] = math.inf
+    w = torch.full((n,), 2.0, device=dev, dtype=dtype)
+    print(f"[gpu] norm of overflowing squares {n} {dtype} {out}", flush=True)
+    codes, scale, _ = fw.add_rms_norm_quant(x, w, out_dtype=out)
+    assert (codes[:2].float() == 0).all() and (scale[:2] == 2.0 ** -126).all() and scale[2].isnan()
+    codes, _, _ = fw.add_rms_norm_quant(x, w, out_dtype=out, scale=torch.tensor([0.01], device=dev))
+    codes = codes.float()
+    assert (codes[:2] == 0).all()
+    here = torch.arange(n, device=dev) == n // 2
+    assert (codes[2, ~here] == 0).all() and (codes[2, n // 2] == 0 if out == torch.int8 else codes[2, n // 2].isnan())
