@@ -14,6 +14,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/core/AutogradState.h>
 #include <c10/core/GradMode.h>
 #include <c10/core/impl/VirtualGuardImpl.h>
 #include <c10/hip/HIPStream.h>
@@ -86,13 +87,25 @@ const Tensor &gpu(const char *name, PyObject *o)
     return THPVariable_Unpack(o);
 }
 
-void no_grad(std::initializer_list<const Tensor *> tensors)
+// Refuses what autograd would lose: a gradient of an input or of an output that
+// is given, and (torch.no_grad leaves those on) a forward-mode tangent.
+// Arguments that are no tensors are refused later, by name.
+void outside_autograd(std::initializer_list<PyObject *> inputs, std::initializer_list<PyObject *> outputs = {})
 {
-    if (!c10::GradMode::is_enabled()) return;
-    for (const Tensor *t : tensors)
-        if (t && t->requires_grad())
-            throw Refusal{PyExc_RuntimeError,
-                          "an input requires a gradient: call under torch.no_grad() and make the backward call"};
+    const bool backward = c10::GradMode::is_enabled(), forward = c10::AutogradState::get_tls_state().get_fw_grad_mode();
+    const auto check = [&](std::initializer_list<PyObject *> objects, const char *what, const char *then) {
+        for (PyObject *o : objects) {
+            if (!THPVariable_Check(o)) continue;
+            const Tensor &t = THPVariable_Unpack(o);
+            if (backward && t.requires_grad())
+                throw Refusal{PyExc_RuntimeError, std::string(what) + " requires a gradient: call under torch.no_grad()" + then};
+            if (forward && t._fw_grad(0).defined())
+                throw Refusal{PyExc_RuntimeError,
+                              std::string(what) + " has a forward-mode tangent, which the call would drop: pass its primal"};
+        }
+    };
+    check(inputs, "an input", " and make the backward call");
+    check(outputs, "an output", "");
 }
 
 void floating(const char *name, const Tensor &t)
@@ -224,15 +237,13 @@ PyObject *tuple(std::initializer_list<PyObject *> items)
     return t;
 }
 
-typedef std::initializer_list<const Tensor *> Tensors;
-
 // x, weight, residual, eps, out_dtype, scale, h_out
 PyObject *add_rms_norm_quant(PyObject *const *a)
 {
+    outside_autograd({a[0], a[1], a[2], a[5]}, {a[6]});
     const Tensor &x = gpu("x", a[0]), &weight = tensor("weight", a[1]);
     const Tensor *residual = optional("residual", a[2]), *scale = optional("scale", a[5]), *given_h = optional("h_out", a[6]);
     const c10::Device dev = x.device();
-    no_grad({&x, &weight, residual});
     floating("x", x);
     floating("weight", weight, x.scalar_type());
     const Rows r = rows("x", x);
@@ -280,10 +291,10 @@ PyObject *add_rms_norm_quant(PyObject *const *a)
 // g, h, weight, eps, grad_h
 PyObject *add_rms_norm_backward(PyObject *const *a)
 {
+    outside_autograd({a[0], a[1], a[2], a[4]});
     const Tensor &g = gpu("g", a[0]), &h = tensor("h", a[1]), &weight = tensor("weight", a[2]);
     const Tensor *grad_h = optional("grad_h", a[4]);
     const c10::Device dev = g.device();
-    no_grad({&g, &h, &weight, grad_h});
     floating("g", g);
     floating("h", h, g.scalar_type());
     floating("weight", weight, g.scalar_type());
@@ -327,6 +338,7 @@ int scale_per_row(const char *name, const Tensor &s, int64_t n, bool column, c10
 // mat1, mat2, scale_a, scale_b, bias, out_dtype, out
 PyObject *int8_scaled_mm(PyObject *const *a)
 {
+    outside_autograd({a[2], a[3], a[4]}, {a[6]});
     const Tensor &x = tensor("mat1", a[0]), &w = tensor("mat2", a[1]);
     if (x.scalar_type() != ScalarType::Char || w.scalar_type() != ScalarType::Char)
         type_error("expected int8 operands, got " + str(x.scalar_type()) + " and " + str(w.scalar_type()));
@@ -346,7 +358,6 @@ PyObject *int8_scaled_mm(PyObject *const *a)
     const Tensor &sa = tensor("scale_a", a[2]), &sb = tensor("scale_b", a[3]);
     const int per_a = scale_per_row("scale_a", sa, M, false, dev), per_b = scale_per_row("scale_b", sb, N, true, dev);
     const Tensor *bias = optional("bias", a[4]), *given = optional("out", a[6]);
-    no_grad({&sa, &sb, bias});
     if (bias) {
         floating("bias", *bias, out_dtype);
         vector("bias", *bias, N, dev);
@@ -407,8 +418,8 @@ c10::SmallVector<int64_t, 6> with_axis(at::IntArrayRef lead, int64_t k)
 // logits, tokens, top_k
 PyObject *token_logprobs(PyObject *const *a)
 {
+    outside_autograd({a[0]});
     const Tensor &logits = gpu("logits", a[0]), &given = tensor("tokens", a[1]);
-    no_grad({&logits});
     floating("logits", logits);
     const Rows r = rows("logits", logits);
     const int64_t C = tokens_of(given, logits);
@@ -436,12 +447,12 @@ PyObject *token_logprobs(PyObject *const *a)
 // logits, tokens, lse, entropy, grad_logprobs, grad_entropy, top_tokens, grad_top, out
 PyObject *token_logprobs_backward(PyObject *const *a)
 {
+    outside_autograd({a[0], a[2], a[3], a[4], a[5], a[7]}, {a[8]});
     const Tensor &logits = gpu("logits", a[0]), &given = tensor("tokens", a[1]), &lse0 = tensor("lse", a[2]);
     const Tensor *entropy0 = optional("entropy", a[3]), *g0 = optional("grad_logprobs", a[4]),
                  *ge0 = optional("grad_entropy", a[5]), *top0 = optional("top_tokens", a[6]), *gt0 = optional("grad_top", a[7]),
                  *given_out = optional("out", a[8]);
     const c10::Device dev = logits.device();
-    no_grad({&logits, &lse0, entropy0, g0, ge0, gt0});
     floating("logits", logits);
     const Rows r = rows("logits", logits);
     const int64_t C = tokens_of(given, logits);

@@ -61,3 +61,41 @@ def test_norm_rows_whose_squares_overflow(dev, n, dtype, out):
     assert (codes[:2] == 0).all()
     here = torch.arange(n, device=dev) == n // 2
     assert (codes[2, ~here] == 0).all() and (codes[2, n // 2] == 0 if out == torch.int8 else codes[2, n // 2].isnan())
+
+
+# ---- autograd: what a call would lose is refused (no GPU: before any other check) ----
+def calls_of(make):
+    """Every call with make() in the place of each of its floating arguments in turn, by name."""
+    z, w, one = torch.zeros(4, 64), torch.ones(64), torch.ones(1)
+    i8, tok, row = torch.zeros(4, 64, dtype=torch.int8), torch.zeros(4, dtype=torch.int64), torch.zeros(4)
+    top = torch.zeros(4, 2, dtype=torch.int64)
+    calls = [
+        (fw.add_rms_norm_quant, dict(x=z, weight=w, residual=z, scale=one, h_out=z), ()),
+        (fw.add_rms_norm_backward, dict(g=z, h=z, weight=w, grad_h=z), ()),
+        (fw.int8_scaled_mm, dict(scale_a=one, scale_b=one, bias=w, out=torch.zeros(4, 64)),
+         dict(mat1=i8, mat2=torch.zeros(64, 64, dtype=torch.int8).t(), out_dtype=torch.float32)),
+        (fw.token_logprobs, dict(logits=z), dict(tokens=tok)),
+        (fw.token_logprobs_backward, dict(logits=z, lse=row, entropy=row, grad_logprobs=row, grad_entropy=row,
+                                          grad_top=torch.zeros(4, 2), out=z), dict(tokens=tok, top_tokens=top)),
+    ]
+    for call, floats, others in calls:
+        for name in floats:
+            yield f"{call.__name__}({name})", lambda: call(**{**floats, name: make(floats[name])}, **dict(others))
+
+
+def test_gradients_that_would_be_lost_are_refused():
+    for name, call in calls_of(lambda t: t.clone().requires_grad_()):
+        with pytest.raises(RuntimeError, match="requires a gradient"):
+            call()
+            pytest.fail(name)
+        with torch.no_grad(), pytest.raises((ValueError, TypeError)):  # (host tensors)
+            call()
+
+
+def test_tangents_that_would_be_lost_are_refused():
+    from torch.autograd import forward_ad
+    with forward_ad.dual_level():
+        for name, call in calls_of(lambda t: forward_ad.make_dual(t.clone(), torch.ones_like(t))):
+            with torch.no_grad(), pytest.raises(RuntimeError, match="tangent"):
+                call()
+                pytest.fail(name)
