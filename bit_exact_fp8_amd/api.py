@@ -179,7 +179,8 @@ def scaled_mm(mat1: torch.Tensor, mat2: torch.Tensor, scale_a: torch.Tensor, sca
     if out_dtype not in OUT_DTYPE:
         raise EmuError(EMU_ERR_UNSUPPORTED, f"output dtype {out_dtype} is not supported")
     dev = x.device
-    if out is None:
+    given = out is not None
+    if not given:
         out = torch.empty((M, N), dtype=out_dtype, device=dev)
     else:
         _on_device("out", out, dev)
@@ -195,6 +196,8 @@ def scaled_mm(mat1: torch.Tensor, mat2: torch.Tensor, scale_a: torch.Tensor, sca
                              _scale_ptr(scale_a, dev), _scale_ptr(scale_b, dev), sr, out.data_ptr(),
                              OUT_DTYPE[out_dtype], ldo, int(use_fast_accum), int(split_S),
                              PROFILE[profile], wsbuf.data_ptr(), ws, _stream_handle(dev), plan))
+    if given:
+        torch.autograd.graph.increment_version(out)   # for autograd, as torch's own operators do
     return out
 
 
@@ -221,6 +224,7 @@ def scaled_mm_noalloc(mat1: torch.Tensor, mat2: torch.Tensor, scale_a: torch.Ten
                                         _scale_ptr(scale_a, dev), _scale_ptr(scale_b, dev), sr, out.data_ptr(),
                                         OUT_DTYPE[out.dtype], ldo, int(use_fast_accum), int(split_S),
                                         PROFILE[profile], _stream_handle(dev), plan_options(tile, defer)))
+    torch.autograd.graph.increment_version(out)
     return out
 
 

@@ -207,6 +207,13 @@ void launch(c10::Device device, F f)
     if (s != EMU_OK) throw Refusal{g_emu_error, emu_last_error_message(), s};
 }
 
+// Autograd is told that a call has written `t`, as for torch's own operators
+// (a tensor of inference mode counts no versions, and nothing saves one).
+void written(const Tensor &t)
+{
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // ---- the calls ----
 
 PyObject *wrap(const Tensor &t)
@@ -285,6 +292,7 @@ PyObject *add_rms_norm_quant(PyObject *const *a)
                                       ptr(codes), code(codes), r.n, as<float>(scale), as<float>(own),
                                       given_h ? ptr(given_h) : ptr(h), ldh, stream);
     });
+    if (given_h) written(*given_h);
     return tuple({wrap(codes), scale ? held(a[5]) : wrap(own), given_h ? held(a[6]) : wrap(h)});
 }
 
@@ -383,6 +391,7 @@ PyObject *int8_scaled_mm(PyObject *const *a)
                                   bias ? code(*bias) : EMU_DT_BF16, given ? ptr(given) : ptr(out),
                                   static_cast<emu_dtype>(code_of(out_dtype)), ldo, ptr(ws), bytes, stream);
     });
+    if (given) written(*given);
     return given ? held(a[6]) : wrap(out);
 }
 
@@ -485,6 +494,7 @@ PyObject *token_logprobs_backward(PyObject *const *a)
                                            as<float>(entropy), as<float>(g), as<float>(ge), as<int64_t>(top), as<float>(gt), k,
                                            given_out ? ptr(given_out) : ptr(out), ldo, stream);
     });
+    if (given_out) written(*given_out);
     return given_out ? held(a[8]) : wrap(out);
 }
 

@@ -10,7 +10,7 @@ import pytest
 import torch
 
 import bit_exact_fp8_amd as fw
-from bit_exact_fp8_amd import build
+from bit_exact_fp8_amd import api, build
 
 ELEMENT = {"float": 4, "half": 2, "bfloat": 2}
 
@@ -99,3 +99,40 @@ def test_tangents_that_would_be_lost_are_refused():
             with torch.no_grad(), pytest.raises(RuntimeError, match="tangent"):
                 call()
                 pytest.fail(name)
+
+
+# ---- outputs that are given: autograd is told that they were written -----------
+def writers(dev):
+    """(name, a tensor to write, the call that does)"""
+    z, w, one = torch.zeros(16, 64, device=dev), torch.ones(64, device=dev), torch.ones(1, device=dev)
+    i8, row, tok = torch.zeros(16, 64, dtype=torch.int8, device=dev), torch.zeros(16, device=dev), torch.zeros(16, dtype=torch.int64, device=dev)
+    f8 = i8.view(torch.float8_e4m3fn)
+    yield "h_out", z.clone(), lambda t: fw.add_rms_norm_quant(z, w, t, h_out=t)
+    yield "int8 out", z.clone()[:, :16], lambda t: fw.int8_scaled_mm(i8, i8.t(), one, one, out_dtype=torch.float32, out=t)
+    yield "gradient's out", z.clone(), lambda t: fw.token_logprobs_backward(t, tok, row, row, row, out=t)
+    yield "fp8 out", z.clone()[:, :16], lambda t: fw.scaled_mm(f8, f8.t(), one, one, out_dtype=torch.float32, out=t)
+    yield "fp8 out, no allocation", z.clone()[:, :16], lambda t: api.scaled_mm_noalloc(f8, f8.t(), one, one, t)
+
+
+@pytest.mark.gpu
+def test_written_outputs_count_a_version(dev):
+    for name, t, call in writers(dev):
+        print(f"[gpu] {name}", flush=True)
+        version = t._version
+        call(t)
+        assert t._version == version + 1, name
+        # what autograd has saved of it is noticed at the backward pass
+        leaf = torch.ones(t.shape, device=dev, requires_grad=True)
+        y = (leaf * t).sum()
+        with torch.no_grad():
+            call(t)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward()
+        version = t._version
+        with pytest.raises((ValueError, TypeError, RuntimeError)):
+            call(t[:, ::2])
+        assert t._version == version, name
+        with torch.inference_mode():  # such a tensor has no version, and autograd saves none
+            u = t.clone()
+            call(u)
+        call(u)
