@@ -623,12 +623,14 @@ __global__ __launch_bounds__(kThreads) void logp_grad_rows(LogpGradParams p, int
     const float ge = p.ge ? p.ge[t] : 0.0f;
 
     float part = 0.0f;
+    bool beyond = false;
     for (int j = threadIdx.x & 63; j < H; j += 64) {  // every wave adds all of them, in the same order
         const bool given = j < p.C;
         const int64_t v = given ? p.tokens[t * p.C + j] : p.top_tok[t * p.k + (j - p.C)];
         float x = given ? (p.g ? p.g[t * p.C + j] : 0.0f) : p.gtop[t * p.k + (j - p.C)];
         if (v < 0) x = 0.0f;
         if (v >= p.V) x = __uint_as_float(0x7FC00000u);
+        beyond |= v >= p.V;
         part += x;
         if (threadIdx.x < 64) {
             const bool here = v >= s0 && v < s1;
@@ -641,7 +643,7 @@ __global__ __launch_bounds__(kThreads) void logp_grad_rows(LogpGradParams p, int
     float A = -total;
     if (p.ge) A -= ge * p.entropy[t];
     if (lse != lse) A = lse;
-    const bool empty = lse == -INFINITY;
+    const bool empty = lse == -INFINITY && !__any(beyond);
     const auto value = [&](float x) {
         const float d = fmaxf(x - lse, kFar);
         float e = exp_of(d);

@@ -148,7 +148,8 @@ EMU_API size_t emu_token_logprobs_workspace(int64_t T, int64_t V, int64_t top_k)
  * itself is not taken.  lse and entropy are the forward call's.  grad [T, V]
  * is of the logits' type and may be the logits themselves.  Where a logit is
  * -inf its p and p lp are 0.  A row whose lse is -inf gets zeros.  A token or
- * top token of V or more, as a NaN in lse, gives its row NaN.
+ * top token of V or more, as a NaN in lse, gives its row NaN (also one whose
+ * lse is -inf).
  */
 EMU_API emu_status emu_token_logprobs_backward(const void *logits, emu_dtype z_dtype, int64_t ldz,
                                                int64_t T, int64_t V, const int64_t *tokens, int64_t C,

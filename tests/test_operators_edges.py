@@ -11,6 +11,7 @@ import torch
 
 import bit_exact_fp8_amd as fw
 from bit_exact_fp8_amd import api, build
+from test_operators import check_logp_grad
 
 ELEMENT = {"float": 4, "half": 2, "bfloat": 2}
 
@@ -136,3 +137,18 @@ def test_written_outputs_count_a_version(dev):
             u = t.clone()
             call(u)
         call(u)
+
+
+# ---- token log probabilities ------------------------------------------------
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [50, 9001])
+def test_tokens_out_of_the_vocabulary_give_nan_in_empty_rows_too(dev, V, dtype):
+    """A row of nothing but -inf has the gradient 0, but a token (or top token)
+    of V or more gives its row NaN, whatever the logits."""
+    z = torch.full((5, V), -math.inf, dtype=dtype)
+    tokens = torch.tensor([[2, V], [2, V - 1], [-1, 1 << 40], [2, 2], [-1, -1]])
+    top = torch.tensor([[1], [V], [1], [1], [0]])
+    ones = torch.ones(5, 2)
+    check_logp_grad(dev, z, tokens, ones, torch.ones(5), top, ones[:, :1])
+    check_logp_grad(dev, z, tokens, ones * math.inf, None, None, None)
