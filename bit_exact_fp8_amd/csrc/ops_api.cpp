@@ -243,7 +243,7 @@ emu_status emu_token_logprobs_backward(const void *logits, emu_dtype z_dtype, in
     if (T > kMaxRows || V > INT32_MAX - 4096) return unsupported("T above 2^31-1 or V above 2^31-4097");
     if (!g) C = 0;
     if (!g_top) top_k = 0;
-    if (C > emu::kMaxGradTokens || top_k > emu::kMaxGradTokens - C) return unsupported("C + top_k above 1024");
+    if (C > emu::kMaxGradTokens || top_k > emu::kMaxGradTokens - C) return unsupported("C + top_k above EMU_MAX_GRAD_TOKENS (1024)");
     if (T == 0 || V == 0) return set_error(EMU_OK, "");
     if (!logits || !lse || !grad || (C > 0 && !tokens) || (top_k > 0 && !top_tokens) || (g_entropy && !entropy))
         return invalid("null pointer");

@@ -86,7 +86,7 @@ struct LogpGradParams {
     void *grad;
     int64_t ldgrad;
 };
-constexpr int64_t kMaxGradTokens = 1024;  // C + top_k: their tokens and values are kept in LDS
+constexpr int64_t kMaxGradTokens = EMU_MAX_GRAD_TOKENS;  // C + top_k: their tokens and values are kept in LDS
 hipError_t launch_logp_grad(int z_dtype, const LogpGradParams &p, hipStream_t stream);
 
 // Sets this thread's error text (emu_last_error_message) and returns s.

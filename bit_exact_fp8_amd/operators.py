@@ -8,9 +8,10 @@ tokens with entropy and top alternatives, and their gradient.
 
 As in ``api``: argument checks and marshalling only (compiled, in
 ``csrc/ops_binding.cpp``), every step runs in the HIP library's kernels on
-torch's current stream of the operands' device, and there is no CPU fallback.  Calls take no part in autograd: the backward calls
-are the caller's to make, and an input that requires a gradient is refused
-while gradients are enabled.
+torch's current stream of the operands' device, and there is no CPU fallback.
+Calls take no part in autograd: the backward calls are the caller's to make,
+an input or a given output that requires a gradient is refused while gradients
+are enabled, and one with a forward-mode tangent always.
 """
 from __future__ import annotations
 
@@ -22,6 +23,7 @@ import torch
 from . import api
 
 MAX_TOP_TOKENS = 64          # EMU_MAX_TOP_TOKENS
+MAX_GRAD_TOKENS = 1024       # EMU_MAX_GRAD_TOKENS
 
 _LIB = None
 
@@ -122,8 +124,10 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top_k: int = 0) -
     logits [..., V]; tokens int64 [...] or [..., C], a token below 0 standing
     for none (its log probability is 0).  All outputs are float32, in the
     natural logarithm; top_tokens int64, in falling order, equal logits by
-    rising token; top_k <= min(V, 64).  Logits of -inf have probability 0; a
-    row of nothing else has lse and log probabilities -inf and entropy 0."""
+    rising token; top_k <= min(V, MAX_TOP_TOKENS).  Logits of -inf have
+    probability 0; a row of nothing else has lse and log probabilities -inf and
+    entropy 0.  Any number of tokens a row; the backward call takes
+    MAX_GRAD_TOKENS."""
     return TokenLogprobs(*(_OPS or _binding()).token_logprobs(logits, tokens, top_k))
 
 
@@ -135,7 +139,8 @@ def token_logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor, lse: tor
     ``token_logprobs``'s outputs (each may be None).
 
     lse and entropy are the forward call's, and so is top_tokens where
-    grad_top is given; entropy may be None where grad_entropy is.  out: where
-    to write it, which may be the logits themselves."""
+    grad_top is given; entropy may be None where grad_entropy is.  A row's
+    gradients of tokens and of alternatives are at most MAX_GRAD_TOKENS (1024)
+    together.  out: where to write it, which may be the logits themselves."""
     return (_OPS or _binding()).token_logprobs_backward(logits, tokens, lse, entropy, grad_logprobs, grad_entropy,
                                                          top_tokens, grad_top, out)

@@ -138,6 +138,9 @@ EMU_API emu_status emu_token_logprobs(const void *logits, emu_dtype z_dtype, int
                                       void *workspace, size_t workspace_bytes, hipStream_t stream);
 EMU_API size_t emu_token_logprobs_workspace(int64_t T, int64_t V, int64_t top_k);
 
+/* The most tokens and alternatives that a row's gradient can come from. */
+#define EMU_MAX_GRAD_TOKENS 1024
+
 /*
  * The gradient of a loss that reads emu_token_logprobs's outputs: with
  * g [T, C] that of logprobs, g_entropy [T] that of the entropy and g_top
@@ -149,7 +152,8 @@ EMU_API size_t emu_token_logprobs_workspace(int64_t T, int64_t V, int64_t top_k)
  * is of the logits' type and may be the logits themselves.  Where a logit is
  * -inf its p and p lp are 0.  A row whose lse is -inf gets zeros.  A token or
  * top token of V or more, as a NaN in lse, gives its row NaN (also one whose
- * lse is -inf).
+ * lse is -inf).  C (if g is given) and top_k (if g_top is) are at most
+ * EMU_MAX_GRAD_TOKENS together; the forward call takes any C.
  */
 EMU_API emu_status emu_token_logprobs_backward(const void *logits, emu_dtype z_dtype, int64_t ldz,
                                                int64_t T, int64_t V, const int64_t *tokens, int64_t C,

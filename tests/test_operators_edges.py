@@ -10,7 +10,7 @@ import pytest
 import torch
 
 import bit_exact_fp8_amd as fw
-from bit_exact_fp8_amd import api, build
+from bit_exact_fp8_amd import api, build, operators
 from test_operators import check_logp_grad
 
 ELEMENT = {"float": 4, "half": 2, "bfloat": 2}
@@ -152,3 +152,17 @@ def test_tokens_out_of_the_vocabulary_give_nan_in_empty_rows_too(dev, V, dtype):
     ones = torch.ones(5, 2)
     check_logp_grad(dev, z, tokens, ones, torch.ones(5), top, ones[:, :1])
     check_logp_grad(dev, z, tokens, ones * math.inf, None, None, None)
+
+
+def test_limits_are_the_headers():
+    """The limits that Python names are the header's, and where the calls refuse."""
+    with open(os.path.join(build.ROOT, "include", "emu_operators.h")) as f:
+        named = dict(re.findall(r"#define EMU_(MAX_\w+) (\d+)\n", f.read()))
+    assert named == {"MAX_TOP_TOKENS": str(operators.MAX_TOP_TOKENS), "MAX_GRAD_TOKENS": str(operators.MAX_GRAD_TOKENS)}
+    lib, most = operators._lib(), operators.MAX_GRAD_TOKENS
+    for C, k, status in ((most, 0, 0), (most + 1, 0, 3), (most - 64, 64, 0), (most - 63, 64, 3)):
+        assert lib.emu_token_logprobs_backward(16, 0, 100, 0, 100, 16, C, 16, None, 16, None, 16, 16 if k else None, k, 16, 100,
+                                               None) == status
+    assert lib.emu_token_logprobs_backward(16, 0, 100, 0, 100, 16, most + 1, 16, 16, None, 16, None, None, 0, 16, 100, None) == 0
+    for k, status in ((operators.MAX_TOP_TOKENS, 0), (operators.MAX_TOP_TOKENS + 1, 3)):
+        assert lib.emu_token_logprobs(16, 0, 100, 0, 100, 16, 1, k, 16, 16, 16, 16, 16, None, 0, None) == status
