@@ -11,7 +11,8 @@ import torch
 
 import bit_exact_fp8_amd as fw
 from bit_exact_fp8_amd import api, build, operators
-from test_operators import check_logp_grad
+from test_operators import (BF, E4, E5, F, HF, I8, MOST, SF, check_logp, check_logp_grad, check_norm, check_norm_grad, close,
+                            f64, half_step, make_logits, norm64, rand, rng)
 
 ELEMENT = {"float": 4, "half": 2, "bfloat": 2}
 
@@ -166,3 +167,109 @@ def test_limits_are_the_headers():
     assert lib.emu_token_logprobs_backward(16, 0, 100, 0, 100, 16, most + 1, 16, 16, None, 16, None, None, 0, 16, 100, None) == 0
     for k, status in ((operators.MAX_TOP_TOKENS, 0), (operators.MAX_TOP_TOKENS + 1, 3)):
         assert lib.emu_token_logprobs(16, 0, 100, 0, 100, 16, 1, k, 16, 16, 16, 16, 16, None, 0, None) == status
+
+
+# ---- paths that only large or unusual calls take -----------------------------
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,n,x_t,r_t,out,given", [(14001, 2057, BF, BF, E4, True), (4501, 4071, BF, SF, I8, False),
+                                                   (26003, 801, SF, SF, E5, False), (3001, 9001, HF, SF, E4, True)])
+def test_norm_past_the_cache(dev, T, n, x_t, r_t, out, given):
+    """Calls of more than 192 MiB, which pass by the last-level cache."""
+    check_norm(dev, T, n, x_t, r_t, out, given)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,n,g_t,h_t,gh_t", [(9001, 2807, BF, BF, BF), (3501, 3607, SF, SF, SF), (24001, 701, HF, SF, SF),
+                                              (1801, 9007, BF, SF, SF)])
+def test_norm_grad_past_the_cache(dev, T, n, g_t, h_t, gh_t):
+    check_norm_grad(dev, T, n, g_t, h_t, gh_t, g_t)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,V,dtype,k", [(3301, 30503, HF, 0), (2003, 26003, SF, 0), (1501, 34001, SF, 4)])
+def test_logp_past_the_cache(dev, T, V, dtype, k):
+    gen = rng(V)
+    z, tokens = make_logits(gen, T, V, dtype), torch.randint(-1, V, (T, 1), generator=gen)
+    at = "cpu" if k else dev  # (where the definition is computed)
+    check_logp(dev, z.to(at), tokens.to(at), k)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,V,dtype", [(1701, 30503, HF), (1003, 26003, SF)])
+def test_logp_grad_past_the_cache(dev, T, V, dtype):
+    gen = rng(V)
+    z, tokens = make_logits(gen, T, V, dtype), torch.randint(-1, V, (T, 1), generator=gen)
+    check_logp_grad(dev, z, tokens, rand(gen, T, 1), rand(gen, T), None, None, inplace=True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,pad", [(3, 0), (9, 3)])
+def test_norm_of_more_rows_than_a_launch(dev, n, pad):
+    check_norm(dev, 2 ** 20 + 3, n, BF, SF, I8, False, pad=pad)
+    check_norm(dev, 2 ** 20 + 3, n, HF, None, E4, True, pad=pad)
+
+
+@pytest.mark.gpu
+def test_logp_of_more_rows_than_a_launch(dev):
+    gen = rng(20)
+    T = 2 ** 20 + 3
+    check_logp(dev, make_logits(gen, T, 5, BF), torch.randint(-1, 6, (T, 2), generator=gen), 2, pad=2)
+    T = 2 ** 23 + 3
+    check_logp_grad(dev, make_logits(gen, T, 2, HF), torch.randint(-1, 2, (T, 1), generator=gen), rand(gen, T, 1), None, None, None)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,V,k", [(3, 5000, 3), (2, 50001, 0), (513, 700, 2)])
+def test_logp_of_more_tokens_than_threads(dev, T, V, k):
+    """More than 256 tokens a row, of rows that are split and of whole ones."""
+    gen = rng(V)
+    check_logp(dev, make_logits(gen, T, V, SF), torch.randint(-1, V + 1, (T, 700), generator=gen), k)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("where", ["g", "grad_h"])
+@pytest.mark.parametrize("T,n", [(5, 5), (40, 77), (700, 1925), (9, 9000), (3, 12001), (300, 17003)])
+@pytest.mark.parametrize("dtype", [BF, SF])
+def test_norm_grad_in_place(dev, T, n, dtype, where):
+    """grad_in may be g or grad_h itself: the same bits as into another tensor."""
+    gen = rng(n)
+    g, h, gh = (rand(gen, T, n + 1, dtype=dtype).to(dev) for _ in range(3))
+    w = rand(gen, n, dtype=dtype).to(dev)
+    print(f"[gpu] norm gradient in place of {where} {T}x{n} {dtype}", flush=True)
+    want, want_w = fw.add_rms_norm_backward(g[:, :n], h[:, :n], w, grad_h=gh[:, :n])
+    lib, code, ld = operators._lib(), 0 if dtype == BF else 2, n + 1
+    out, grad_w = (g if where == "g" else gh), torch.empty_like(w)
+    need = lib.emu_add_rms_norm_backward_workspace(T, n)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    status = lib.emu_add_rms_norm_backward(g.data_ptr(), code, ld, h.data_ptr(), code, ld, w.data_ptr(), code, gh.data_ptr(), code,
+                                           ld, T, n, 1e-6, out.data_ptr(), ld, grad_w.data_ptr(), ws.data_ptr(), need,
+                                           torch.cuda.current_stream(dev).cuda_stream)
+    torch.cuda.synchronize(dev)
+    assert status == 0 and torch.equal(out[:, :n], want) and torch.equal(grad_w, want_w)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("out", [E4, E5, I8])
+@pytest.mark.parametrize("n", [40, 2000, 20000])
+@pytest.mark.parametrize("given", [None, 2.0 ** -118, 2.0 ** -125])
+def test_norm_of_very_small_weights(dev, n, out, given):
+    """Scales under 2^-100.  y is made by two products in binary32, which near
+    2^-126 are off by up to 2^-150 each whatever their size."""
+    gen = rng(n)
+    x = rand(gen, 4, n)
+    w = (1 + torch.rand(n, generator=gen)) * torch.exp2(-112 - torch.randint(0, 20, (n,), generator=gen).float())
+    w[0] = 2.0 ** -111
+    x[:, 0] = 2.0
+    print(f"[gpu] norm of small weights {n} {out} given={given}", flush=True)
+    codes, scale, _ = fw.add_rms_norm_quant(x.to(dev), w.to(dev), out_dtype=out,
+                                            scale=None if given is None else torch.tensor([given], device=dev))
+    _, y = norm64(x, None, w, 1e-6)
+    if given is None:
+        want = (y.abs().amax(1, keepdim=True) / MOST[out]).clamp_min(2.0 ** -126)
+        assert float(want.max()) < 2.0 ** -100
+        # (three products and a quotient, the first of them possibly below 2^-126)
+        close(scale, want, want * F, "scale")
+    s = scale.cpu().to(f64)
+    z = (y / s).clamp(-MOST[out], MOST[out])
+    step = torch.full_like(z, 0.5) if out == I8 else half_step(z, out)
+    close(codes.cpu().float(), z, step + z.abs() * F + 2.0 ** -149 / s, "codes")
