@@ -253,35 +253,29 @@ __global__ __launch_bounds__(WM * WN * 64, BM * BN >= 128 * 128 ? 2 : 4) void in
     const auto half = [&](int s, auto which, int buf, int next, bool whole) {
         constexpr int h = decltype(which)::value, o = h ^ 1;
         __builtin_amdgcn_sched_barrier(0);
-        constexpr int R0 = 0;                        // rows multiplied before the wait
-        constexpr int NW = (FN + FM - R0 - 1) / (FM - R0);              // fragments of w to read with a row
-        constexpr int T0 = R0 * FN;
+        constexpr int NW = (FN + FM - 1) / FM;       // fragments of w to read with a row
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
-            if (h && i == R0) {
+            if (h && i == 0) {
                 __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave has read buffer s
                 wait_loads<(NB - 2) * LPW>();
                 __builtin_amdgcn_s_barrier();
                 __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                for (int x = 0; x < R0; ++x) A[x] = *reinterpret_cast<const i32x4 *>(fa[o] + next * BUF + x * 16 * kStage);
             }
-            if (i >= R0) {
 #pragma unroll
-                for (int x = (i - R0) * NW; x < (i - R0 + 1) * NW && x < FN; ++x)
-                    B[o][x] = *reinterpret_cast<const i32x4 *>(fw[o] + next * BUF + x * 16 * kStage);
-            }
+            for (int x = i * NW; x < (i + 1) * NW && x < FN; ++x)
+                B[o][x] = *reinterpret_cast<const i32x4 *>(fw[o] + next * BUF + x * 16 * kStage);
 #pragma unroll
             for (int j = 0; j < FN; ++j) {
-                const int t = i * FN + j - T0;
-                if (h && t >= 0) {
+                const int t = i * FN + j;
+                if (h) {
 #pragma unroll
-                    for (int q = t * LPW / (T - T0); q < (t + 1) * LPW / (T - T0); ++q) load(q, s + NB, buf, whole);
+                    for (int q = t * LPW / T; q < (t + 1) * LPW / T; ++q) load(q, s + NB, buf, whole);
                 }
                 acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(B[h][j], A[i], acc[i][j], 0, 0, 0);
                 __builtin_amdgcn_sched_barrier(0);
             }
-            if (i >= R0) A[i] = *reinterpret_cast<const i32x4 *>(fa[o] + next * BUF + i * 16 * kStage);
+            A[i] = *reinterpret_cast<const i32x4 *>(fa[o] + next * BUF + i * 16 * kStage);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
