@@ -164,10 +164,11 @@ __device__ __forceinline__ void tile_of(int id, int tm, int tn, int &m, int &n)
     n = in / high;
 }
 
-// part: null, or [S, M, N] sums of each K split (grid y).
+// part: null, or [S, M, N] sums of each K split (grid y).  The launch bounds
+// ask for the waves a SIMD that the stages in LDS leave room for, at most 2.
 template <int BM, int BN, int WM, int WN, int NB>
-__global__ __launch_bounds__(WM * WN * 64, BM * BN >= 128 * 128 ? 2 : 4) void int8_tiles(Int8Params p, int tm, int tn, int stages,
-                                                                                int *part)
+__global__ __launch_bounds__(WM * WN * 64, NB * (BM + BN) * kStage * 2 <= 160 * 1024 || WM * WN > 4 ? 2 : 1) void int8_tiles(
+    Int8Params p, int tm, int tn, int stages, int *part)
 {
     constexpr int FM = BM / WM / 16, FN = BN / WN / 16;           // fragments of a wave, in a half
     constexpr int LPW = (BM + BN) / 8 / (WM * WN);                // its loads a stage, 8 rows each
