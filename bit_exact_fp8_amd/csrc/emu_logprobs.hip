@@ -435,7 +435,7 @@ __global__ __launch_bounds__(kThreads, HELD ? 6 : 8) void logp_rows(LogpParams p
         }
         take16(a, x, y, most);
     };
-    f32x8 x, y;
+    f32x8 x{}, y{};  // (only HELD uses them)
     if constexpr (HELD) {
         x = logits8(z, c0, s1);
         y = logits8(z, c0 + kTile, s1);
