@@ -95,7 +95,7 @@ void outside_autograd(std::initializer_list<PyObject *> inputs, std::initializer
     const bool backward = c10::GradMode::is_enabled(), forward = c10::AutogradState::get_tls_state().get_fw_grad_mode();
     const auto check = [&](std::initializer_list<PyObject *> objects, const char *what, const char *then) {
         for (PyObject *o : objects) {
-            if (!THPVariable_Check(o)) continue;
+            if (o == Py_None || !THPVariable_Check(o)) continue;  // (None takes that check the long way: 0.3 us of a 5 us call)
             const Tensor &t = THPVariable_Unpack(o);
             if (backward && t.requires_grad())
                 throw Refusal{PyExc_RuntimeError, std::string(what) + " requires a gradient: call under torch.no_grad()" + then};

@@ -107,7 +107,8 @@ def test_tangents_that_would_be_lost_are_refused():
 def writers(dev):
     """(name, a tensor to write, the call that does)"""
     z, w, one = torch.zeros(16, 64, device=dev), torch.ones(64, device=dev), torch.ones(1, device=dev)
-    i8, row, tok = torch.zeros(16, 64, dtype=torch.int8, device=dev), torch.zeros(16, device=dev), torch.zeros(16, dtype=torch.int64, device=dev)
+    i8, row = torch.zeros(16, 64, dtype=torch.int8, device=dev), torch.zeros(16, device=dev)
+    tok = torch.zeros(16, dtype=torch.int64, device=dev)
     f8 = i8.view(torch.float8_e4m3fn)
     yield "h_out", z.clone(), lambda t: fw.add_rms_norm_quant(z, w, t, h_out=t)
     yield "int8 out", z.clone()[:, :16], lambda t: fw.int8_scaled_mm(i8, i8.t(), one, one, out_dtype=torch.float32, out=t)
