@@ -104,9 +104,9 @@ __device__ __forceinline__ void finish(const Int8Params &p, int64_t m, int64_t n
 
 // ---- tiles -------------------------------------------------------------
 //
-// 8192^3 takes 430 us (2.56 POP/s; 395 to 445 as the card's power allows, against
-// 4.0 POP/s of matrix instructions alone on such codes, also at the power
-// limit, and 4.8 on zeros).
+// 8192^3 takes 415 us (2.65 POP/s; 370 to 445 as the card's power allows, against
+// 4.4 POP/s of matrix instructions alone on such codes, also at the power
+// limit, and 4.9 on zeros).
 // A workgroup of WM x WN waves makes BM x BN outputs, a stage of 128 codes of
 // K at a time.  Stages come from global memory straight into LDS (16 bytes a
 // lane), NB buffers deep, whole 128-byte lines: a CU takes up to 115 GB/s of

@@ -17,7 +17,8 @@
  * enqueued, and a status other than EMU_OK means that nothing was written.
  * Matrices are row-major with a leading dimension in elements; elements are
  * aligned to their own size, and no more is asked of pointers or leading
- * dimensions.  Results are deterministic: no atomics take part in them.
+ * dimensions.  Results are deterministic: they depend on the order of no
+ * atomic operation.
  * Outputs must not overlap inputs unless a call says so.  Sums, statistics
  * and products are held in binary32 (int32 for int8 products) and rounded
  * once, to nearest even, where they are stored.
@@ -55,7 +56,9 @@ typedef enum {
  * A NaN in a row's y gives that row the scale NaN (scale == NULL) and NaN
  * codes, 0 for int8, which has none; an infinity in v makes y NaN.
  * The squares of v are summed in binary32, in which values beyond 1.8e19
- * overflow: such a row counts as one with an infinite mean (r = 0).
+ * overflow: such a row counts as one with an infinite mean (y = 0).  Those of
+ * values under 1e-19 lose digits and vanish under 4e-23, which shows where eps
+ * is below some 1e-31.
  * n = 0 with T > 0 is refused; T = 0 does nothing.
  */
 EMU_API emu_status emu_add_rms_norm_quant(const void *x, emu_dtype x_dtype, int64_t ldx,
@@ -77,7 +80,9 @@ EMU_API emu_status emu_add_rms_norm_quant(const void *x, emu_dtype x_dtype, int6
  * g's type or fp32; grad_in may be g or (of its type) grad_h itself.
  * grad_weight [n] of weight's type; T = 0 writes zeros to it.  workspace:
  * emu_add_rms_norm_backward_workspace(T, n) bytes, 16-byte aligned, contents
- * on entry and return do not matter.
+ * on entry and return do not matter.  The sums are binary32's: where a row's
+ * sum of squares overflows, r is 0 as in the forward call, and where that of
+ * u h does as well, its grad_in is NaN.
  */
 EMU_API emu_status emu_add_rms_norm_backward(const void *g, emu_dtype g_dtype, int64_t ldg,
                                              const void *h, emu_dtype h_dtype, int64_t ldh,
