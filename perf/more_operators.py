@@ -114,7 +114,7 @@ def _scales(most, out, scale):
     # the least power of two that brings `most` within the type: both largest values are 7/8 of one
     digits, power = torch.frexp(most)
     power = power - (9 if out == "e4m3fn" else 16) + (digits > 0.875)
-    return torch.ldexp(torch.ones_like(most), power.clamp_min(-126))
+    return torch.ldexp(torch.ones_like(most), torch.where(most > 0, power, -126).clamp_min(-126))
 
 
 def _spread(s, n, dim):
