@@ -1,0 +1,89 @@
+"""The operators on 8-bit floating point codes with a scale for each block of
+128 (C ABI in ``include/emu_block_operators.h``).
+
+``block_quant``: codes and scales of activations and weights.
+``swiglu_block_quant`` / ``swiglu_block_backward``: the gated activation with
+its codes, and its gradient from the codes that gate and up were kept in.
+
+A value's code times its block's scale stands for the value.  Codes are
+float8_e4m3fn or float8_e5m2; scales float32, or float8_e8m0fnu, powers of two,
+which lose no digit of a code and which the matrix instructions apply
+themselves.  As for the other operators: argument checks and marshalling only,
+every step runs in the HIP library's kernels on torch's current stream, calls
+take no part in autograd and refuse what they would lose of it.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple
+
+import torch
+
+from . import operators
+
+BLOCK = 128  # EMU_BLOCK
+
+_LIB = None
+
+
+def _lib():
+    global _LIB
+    if _LIB is None:
+        lib = operators._lib()
+        vp, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+        lib.emu_block_quant.argtypes = [vp, i32, i64, i64, i64, i64, i64, i32, vp, i32, vp, i32, vp]
+        lib.emu_swiglu_block_quant.argtypes = [vp, i64, vp, i64, i32, i64, i64, vp, i32, vp, i32, vp, vp, vp]
+        lib.emu_swiglu_block_backward.argtypes = [vp, i32, i64, vp, i32, vp, i32, i64, i64, vp, i64, vp]
+        _LIB = lib
+    return _LIB
+
+
+_OPS = None
+
+
+def _binding():
+    global _OPS
+    if _OPS is None:
+        _OPS = operators._binding()
+    return _OPS
+
+
+def block_quant(x: torch.Tensor, block_rows: int = 1, out_dtype=torch.float8_e4m3fn, scale_dtype=torch.float8_e8m0fnu):
+    """(codes, scale) of ``x`` in blocks of ``block_rows`` x 128 along the last axis.
+
+    block_rows 1, for activations: x [..., n], scale [..., blocks of n].
+    block_rows 128, for weights: x [N, K] or [E, N, K], scale [(E,) blocks of N,
+    blocks of K].  A block's scale is max(largest |x| / the type's largest,
+    2^-126) in float32, or the least power of two that brings the block within
+    the type; codes are the nearest to x / scale, ties to even.  A block with an
+    infinity or a NaN has the scale NaN and NaN codes."""
+    return (_OPS or _binding()).block_quant(x, block_rows, out_dtype, scale_dtype)
+
+
+class SwigluCodes(NamedTuple):
+    """What ``swiglu_block_quant`` returns; the last two are None unless they are asked for."""
+    codes: torch.Tensor
+    scale: torch.Tensor
+    kept: torch.Tensor | None
+    kept_scale: torch.Tensor | None
+
+
+def swiglu_block_quant(gate: torch.Tensor, up: torch.Tensor, out_dtype=torch.float8_e4m3fn,
+                       scale_dtype=torch.float8_e8m0fnu, keep: bool = False) -> SwigluCodes:
+    """Codes [..., F] and scales [..., blocks of F] of ``gate / (1 + exp(-gate)) * up``.
+
+    gate, up: [..., F] of one type, in any two places (the halves of one
+    product's output among them).  keep: gate's and up's own codes too, side by
+    side in ``kept`` [..., 2 F], with ``kept_scale`` [..., 2 (blocks of F)]:
+    what ``swiglu_block_backward`` needs, in a quarter of gate's and up's bytes
+    in float32.  Where F is a multiple of 128 both are laid out as
+    ``block_quant`` lays out the two halves side by side."""
+    return SwigluCodes(*(_OPS or _binding()).swiglu_block_quant(gate, up, out_dtype, scale_dtype, keep))
+
+
+def swiglu_block_backward(grad_h: torch.Tensor, kept: torch.Tensor, kept_scale: torch.Tensor) -> torch.Tensor:
+    """The gradients of gate and up, side by side in [..., 2 F] of grad_h's type,
+    from that of ``gate / (1 + exp(-gate)) * up`` and the codes that
+    ``swiglu_block_quant`` kept of both (the rounding of h to 8 bits is passed
+    straight through)."""
+    return (_OPS or _binding()).swiglu_block_backward(grad_h, kept, kept_scale)

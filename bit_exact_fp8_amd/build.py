@@ -6,7 +6,8 @@ chains from incoming accumulators), compiled in parallel and linked with the
 dispatcher, the combine kernel, the deferred-infinity kernels
 (emu_specials.hip), the no-allocation entry point (emu_noalloc.hip), the C
 ABI and the operators beside the product (emu_norm.hip, emu_int8.hip,
-emu_logprobs.hip, ops_api.cpp).  The operators' Python calls (ops_binding.cpp)
+emu_logprobs.hip, ops_api.cpp), those on codes with a scale for each block of
+128 among them (emu_block_*.hip, ops_block_api.cpp).  The operators' Python calls (ops_binding.cpp)
 are a module of their own, _ops.so."""
 from __future__ import annotations
 
@@ -40,7 +41,7 @@ def _units(objdir: str):
              (os.path.join(CSRC, "emu_specials.hip"), os.path.join(objdir, "emu_specials.o"), []),
              (os.path.join(CSRC, "emu_noalloc.hip"), os.path.join(objdir, "emu_noalloc.o"), []),
              (os.path.join(CSRC, "emu_api.cpp"), os.path.join(objdir, "emu_api.o"), [])]
-    for name in ("emu_norm.hip", "emu_int8.hip", "emu_logprobs.hip", "ops_api.cpp"):
+    for name in ("emu_norm.hip", "emu_int8.hip", "emu_logprobs.hip", "ops_api.cpp", "emu_block_quant.hip", "ops_block_api.cpp"):
         # the accumulators of the int8 tiles stay in ordinary registers: the
         # compiler otherwise copies them to and fro in the loop
         extra = ["-mllvm", "-amdgpu-mfma-vgpr-form=true"] if name == "emu_int8.hip" else []

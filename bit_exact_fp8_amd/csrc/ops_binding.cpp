@@ -1,5 +1,5 @@
-// ops_binding.cpp -- the Python side of include/emu_operators.h for torch
-// tensors: argument checks, outputs, workspaces and the call on torch's
+// ops_binding.cpp -- the Python side of include/emu_operators.h and
+// emu_block_operators.h for torch tensors: argument checks, outputs, workspaces and the call on torch's
 // current stream.  Compiled, since a decoded token's call is shorter on the
 // GPU than its checks are in Python (1 x 5760 x 1920 int8: 10.5 us a call with
 // a binding through ctypes, the kernel 5).
@@ -22,7 +22,7 @@
 #include <optional>
 #include <string>
 
-#include "../../include/emu_operators.h"
+#include "../../include/emu_block_operators.h"
 
 namespace {
 
@@ -498,6 +498,126 @@ PyObject *token_logprobs_backward(PyObject *const *a)
     return given_out ? held(a[8]) : wrap(out);
 }
 
+// ---- codes with a scale for each block of 128 ----
+
+int64_t blocks_of(int64_t n) { return (n + EMU_BLOCK - 1) / EMU_BLOCK; }
+bool is_code(ScalarType t) { return t == ScalarType::Float8_e4m3fn || t == ScalarType::Float8_e5m2; }
+bool is_scale(ScalarType t) { return t == ScalarType::Float || t == ScalarType::Float8_e8m0fnu; }
+emu_scale_type scale_code(ScalarType t) { return t == ScalarType::Float ? EMU_SCALE_FP32 : EMU_SCALE_E8M0; }
+void codes(const char *name, const Tensor &t)
+{
+    if (!is_code(t.scalar_type()))
+        type_error(std::string(name) + " must be float8_e4m3fn or float8_e5m2, not " + str(t.scalar_type()));
+}
+void scales(const char *name, const Tensor &t)
+{
+    if (!is_scale(t.scalar_type()))
+        type_error(std::string(name) + " must be float32 or float8_e8m0fnu, not " + str(t.scalar_type()));
+}
+void shaped(const char *name, const Tensor &t, at::IntArrayRef shape, c10::Device device)
+{
+    if (t.sizes() != shape) value_error(std::string(name) + " must have shape " + str(shape) + ", not " + str(t.sizes()));
+    on_device(name, t, device);
+}
+void dense(const char *name, const Tensor &t, at::IntArrayRef shape, c10::Device device)
+{
+    shaped(name, t, shape, device);
+    if (!t.is_contiguous()) value_error(std::string(name) + " must be dense");
+}
+bool truth(PyObject *o)
+{
+    const int b = PyObject_IsTrue(o);
+    if (b < 0) {
+        PyErr_Clear();
+        type_error("expected a truth value");
+    }
+    return b != 0;
+}
+
+// x, block_rows, out_dtype, scale_dtype
+PyObject *block_quant(PyObject *const *a)
+{
+    outside_autograd({a[0]});
+    const Tensor &x = gpu("x", a[0]);
+    floating("x", x);
+    const int64_t block_rows = PyLong_AsLongLong(a[1]);
+    if (block_rows == -1 && PyErr_Occurred()) return nullptr;
+    if (block_rows != 1 && block_rows != EMU_BLOCK) value_error("block_rows must be 1 or 128");
+    const ScalarType out = dtype_of(a[2], is_code), scale = dtype_of(a[3], is_scale);
+    c10::SmallVector<int64_t, 6> shape(x.sizes().begin(), x.sizes().end());
+    int64_t E = 1, stride = 0;
+    Rows r{};
+    if (block_rows == 1) {
+        r = rows("x", x);
+    } else {
+        const int64_t dim = x.dim();
+        if (dim != 2 && dim != 3) value_error("x must be a matrix or a batch of them");
+        E = dim == 3 ? x.size(0) : 1;
+        stride = E > 1 ? x.stride(0) : 0;
+        r = {x.size(dim - 2), x.size(dim - 1), x.size(dim - 2) > 1 ? x.stride(dim - 2) : x.size(dim - 1)};
+        if (E > 0 && r.T > 0 && r.n > 1 && x.stride(dim - 1) != 1) value_error("x must have unit stride along its last axis");
+        shape[dim - 2] = blocks_of(r.T);
+    }
+    shape.back() = blocks_of(r.n);
+    const Tensor q = empty(x.sizes(), x, out), s = empty(shape, x, scale);
+    launch(x.device(), [&](hipStream_t stream) {
+        return emu_block_quant(ptr(x), code(x), r.ld, stride, E, r.T, r.n, static_cast<int>(block_rows), ptr(q), code(q), ptr(s),
+                               scale_code(scale), stream);
+    });
+    return tuple({wrap(q), wrap(s)});
+}
+
+// gate, up, out_dtype, scale_dtype, keep
+PyObject *swiglu_block_quant(PyObject *const *a)
+{
+    outside_autograd({a[0], a[1]});
+    const Tensor &gate = gpu("gate", a[0]), &up = tensor("up", a[1]);
+    floating("gate", gate);
+    if (up.scalar_type() != gate.scalar_type()) type_error("up must be of gate's type");
+    const Rows r = rows("gate", gate);
+    const int64_t ldup = same("up", up, gate);
+    const ScalarType out = dtype_of(a[2], is_code), scale = dtype_of(a[3], is_scale);
+    const bool keep = truth(a[4]);
+    c10::SmallVector<int64_t, 6> shape(gate.sizes().begin(), gate.sizes().end());
+    const Tensor q = empty(shape, gate, out);
+    shape.back() = blocks_of(r.n);
+    const Tensor s = empty(shape, gate, scale);
+    Tensor kept, kept_s;
+    if (keep) {
+        shape.back() = 2 * blocks_of(r.n);
+        kept_s = empty(shape, gate, scale);
+        shape.back() = 2 * r.n;
+        kept = empty(shape, gate, out);
+    }
+    launch(gate.device(), [&](hipStream_t stream) {
+        return emu_swiglu_block_quant(ptr(gate), r.ld, ptr(up), ldup, code(gate), r.T, r.n, ptr(q), code(q), ptr(s),
+                                      scale_code(scale), ptr(kept), ptr(kept_s), stream);
+    });
+    return tuple({wrap(q), wrap(s), wrap(kept), wrap(kept_s)});
+}
+
+// grad_h, kept, kept_scale
+PyObject *swiglu_block_backward(PyObject *const *a)
+{
+    outside_autograd({a[0], a[1], a[2]});
+    const Tensor &g = gpu("grad_h", a[0]), &kept = tensor("kept", a[1]), &kept_s = tensor("kept_scale", a[2]);
+    floating("grad_h", g);
+    codes("kept", kept);
+    scales("kept_scale", kept_s);
+    const Rows r = rows("grad_h", g);
+    c10::SmallVector<int64_t, 6> shape(g.sizes().begin(), g.sizes().end());
+    shape.back() = 2 * blocks_of(r.n);
+    dense("kept_scale", kept_s, shape, g.device());
+    shape.back() = 2 * r.n;
+    dense("kept", kept, shape, g.device());
+    const Tensor grad = empty(shape, g, g.scalar_type());
+    launch(g.device(), [&](hipStream_t stream) {
+        return emu_swiglu_block_backward(ptr(g), code(g), r.ld, ptr(kept), code(kept), ptr(kept_s),
+                                         scale_code(kept_s.scalar_type()), r.T, r.n, ptr(grad), 2 * r.n, stream);
+    });
+    return wrap(grad);
+}
+
 template <PyObject *(*call)(PyObject *const *), int N>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t nargs)
 {
@@ -530,6 +650,9 @@ PyMethodDef g_methods[] = {
     {"int8_scaled_mm", function<int8_scaled_mm, 7>(), METH_FASTCALL, nullptr},
     {"token_logprobs", function<token_logprobs, 3>(), METH_FASTCALL, nullptr},
     {"token_logprobs_backward", function<token_logprobs_backward, 9>(), METH_FASTCALL, nullptr},
+    {"block_quant", function<block_quant, 4>(), METH_FASTCALL, nullptr},
+    {"swiglu_block_quant", function<swiglu_block_quant, 5>(), METH_FASTCALL, nullptr},
+    {"swiglu_block_backward", function<swiglu_block_backward, 3>(), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_ops", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

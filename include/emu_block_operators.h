@@ -1,0 +1,87 @@
+/*
+ * emu_block_operators.h -- C ABI of the operators on 8-bit floating point
+ * codes with a scale for each block of 128, in the same library:
+ *
+ *  - emu_block_quant: the codes and scales of activations (blocks of 1 x 128)
+ *    or of weights (128 x 128);
+ *  - emu_swiglu_block_quant: the gated activation silu(gate) * up with its
+ *    codes and, to be kept for the gradient, those of gate and up, and
+ *    emu_swiglu_block_backward, the gradient from what was kept;
+ *  - emu_block_scaled_mm: the product of such codes, and
+ *    emu_grouped_block_scaled_mm, the same by groups of rows, each with
+ *    weights of its own (experts);
+ *  - emu_block_weight_grad: the gradient of a product's weights, from the
+ *    codes that its input was kept in.
+ *
+ * Conventions are those of emu_operators.h: device pointers owned by the
+ * caller, calls only enqueue kernels on `stream`, arguments are checked on the
+ * host first, elements are aligned to their own size and no more is asked,
+ * results are deterministic, outputs must not overlap inputs.
+ *
+ * Codes are e4m3fn (largest value Q = 448) or e5m2 (57344).  A value's code
+ * times the scale of its block stands for the value; along an axis of n values
+ * there are (n + 127) / 128 blocks, the last of which may be shorter.  Scales
+ * are binary32, or e8m0: one byte b for the power of two 2^(b - 127), 255
+ * for NaN.
+ */
+#ifndef EMU_BLOCK_OPERATORS_H
+#define EMU_BLOCK_OPERATORS_H
+
+#include "emu_operators.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define EMU_BLOCK 128
+
+typedef enum {
+    EMU_SCALE_FP32 = 0,
+    EMU_SCALE_E8M0 = 1
+} emu_scale_type;
+
+/*
+ * Codes and scales of x [E, T, n] (bf16, fp16 or fp32; rows ldx and matrices
+ * x_stride elements apart).  block_rows is 1 (a scale for 128 values of a row)
+ * or 128 (one for 128 x 128 values of a matrix).  With m the largest magnitude
+ * of a block its scale is max(RN32(m / Q), 2^-126), or for e8m0 the least
+ * power of two s >= 2^-126 with m <= s Q; codes are the nearest to x / s, ties
+ * to even.  A block with an infinity or a NaN has the scale NaN and NaN codes.
+ * q [E, T, n] dense; scales [E, (T + block_rows - 1) / block_rows, blocks of
+ * n] dense.  Where a block's m is below 2^-100 a code of fp32 scales may be
+ * that of x / s rounded twice.
+ */
+EMU_API emu_status emu_block_quant(const void *x, emu_dtype x_dtype, int64_t ldx, int64_t x_stride,
+                                   int64_t E, int64_t T, int64_t n, int block_rows,
+                                   void *q, emu_dtype q_dtype, void *scales, emu_scale_type s_type,
+                                   hipStream_t stream);
+
+/*
+ * h = gate / (1 + exp(-gate)) * up, in binary32, as codes q [T, F] and scales
+ * [T, blocks of F] of 1 x 128, as emu_block_quant makes them.  gate and up
+ * [T, F] of one type (bf16, fp16 or fp32).  kept: NULL, or [T, 2 F] for the
+ * codes of gate, then those of up, in each row; kept_scales [T, 2 (blocks of
+ * F)] likewise, each half with blocks of its own.  All of them dense, of
+ * q_dtype and s_type.
+ */
+EMU_API emu_status emu_swiglu_block_quant(const void *gate, int64_t ldgate, const void *up, int64_t ldup,
+                                          emu_dtype dtype, int64_t T, int64_t F,
+                                          void *q, emu_dtype q_dtype, void *scales, emu_scale_type s_type,
+                                          void *kept, void *kept_scales, hipStream_t stream);
+
+/*
+ * The gradient of h above from what was kept (dense): with a and b the values
+ * that gate's and up's codes stand for and p = 1 / (1 + exp(-a)),
+ *   grad[t, i] = g b p (1 + a (1 - p));  grad[t, F + i] = g a p.
+ * g [T, F] bf16, fp16 or fp32; grad [T, 2 F] of g's type.
+ */
+EMU_API emu_status emu_swiglu_block_backward(const void *g, emu_dtype g_dtype, int64_t ldg,
+                                             const void *kept, emu_dtype q_dtype,
+                                             const void *kept_scales, emu_scale_type s_type,
+                                             int64_t T, int64_t F, void *grad, int64_t ldgrad, hipStream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* EMU_BLOCK_OPERATORS_H */

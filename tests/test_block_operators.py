@@ -1,0 +1,429 @@
+"""The operators of include/emu_block_operators.h against their definitions in
+64 bits, and their refusals (on the CPU).
+
+Tolerances, from the arithmetic: codes of given values are exact, and so are
+their scales.  Computed values are held in binary32, each passing through at
+most some 10 operations and a sum through at most 64 additions in a row, each
+off by 2^-24 of its size: F = 80 * 2^-24 of the terms' absolute sum bounds
+them; stored values are rounded once, by half a step."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import bit_exact_fp8_amd as fw
+from bit_exact_fp8_amd import block_operators
+from test_operators import BF, E4, E5, F, HF, I8, INF, SF, close, f64, half_step, note, rand, rng, wide
+
+E8 = torch.float8_e8m0fnu
+MOST = {E4: 448.0, E5: 57344.0}
+LEAST = 2.0 ** -126
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    return torch.device("cuda:0")
+
+
+def blocks(n):
+    return (n + 127) // 128
+
+
+# ---- the definitions ---------------------------------------------------------
+def grid(v, out):
+    """The nearest value of an 8-bit type, ties to even."""
+    bits, low = (3, -6) if out == E4 else (2, -14)
+    e = torch.frexp(v)[1].long() - 1
+    step = torch.exp2((e.clamp_min(low) - bits).to(f64))
+    return torch.round(v / step) * step
+
+
+def scale64(m, out, scale):
+    """The scale of blocks with the largest magnitudes m (exact binary32 values, in 64 bits)."""
+    if scale == SF:
+        # (by a tensor: torch divides by a number through its reciprocal on the GPU)
+        s = (m.float() / torch.full_like(m.float(), MOST[out])).to(f64).clamp_min(LEAST)
+    else:
+        d, e = torch.frexp(m)
+        s = torch.exp2((e - (9 if out == E4 else 16) + (d > 0.875)).to(f64)).clamp_min(LEAST)
+        s = torch.where(m > 0, s, LEAST)  # (frexp gives 0 the exponent 0)
+    return torch.where(m.isfinite(), s, math.nan)
+
+
+def spread(s, T, n, rows):
+    """Each block's scale in its values' places."""
+    s = s.repeat_interleave(128, -1)[..., :n]
+    return s if rows == 1 else s.repeat_interleave(rows, -2)[..., :T, :]
+
+
+def quant64(x, rows, out, scale):
+    """(codes' values, scales) of x [.., T, n]."""
+    x = x.to(f64)
+    T, n = x.shape[-2:]
+    pad = torch.nn.functional.pad(x.abs(), (0, -n % 128, 0, -T % rows))
+    m = pad.unflatten(-1, (-1, 128)).amax(-1).unflatten(-2, (-1, rows)).amax(-2)
+    s = scale64(m, out, scale)
+    y = (x / spread(s, T, n, rows))
+    y = torch.where(y.isnan(), y, y.clamp(-MOST[out], MOST[out]))
+    return torch.where(y.isnan(), y, grid(y, out)), s
+
+
+def same(got, want, what):
+    """The same values, NaN in the same places."""
+    got, want = got.cpu().float().to(f64), want.cpu()
+    assert got.shape == want.shape, (what, got.shape, want.shape)
+    bad = ~((got == want) | (got.isnan() & want.isnan()))
+    assert not bad.any(), (what, int(bad.sum()), bad.nonzero()[:4].tolist(), got[bad][:4], want[bad][:4])
+
+
+def check_quant(dev, x, rows, out, scale, pad=0):
+    note(f"block codes {tuple(x.shape)} {x.dtype} rows={rows} {out} {scale} pad={pad}")
+    xd = wide(x, pad, dev) if x.dim() == 2 else x.to(dev)
+    q, s = fw.block_quant(xd, block_rows=rows, out_dtype=out, scale_dtype=scale)
+    torch.cuda.synchronize(dev)
+    assert q.dtype == out and s.dtype == scale and q.is_contiguous() and s.is_contiguous()
+    want_q, want_s = quant64(x, rows, out, scale)
+    same(s, want_s, "scales")
+    same(q, want_q, "codes")
+
+
+SIZES = [(1, 1), (1, 127), (2, 128), (3, 129), (5, 8), (7, 300), (127, 7), (128, 128), (129, 257), (33, 1925), (300, 1000),
+         (1, 40000), (1000, 64), (513, 2048)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,n", SIZES)
+@pytest.mark.parametrize("rows", [1, 128])
+@pytest.mark.parametrize("dtype,out,scale", [(BF, E4, E8), (HF, E5, SF), (SF, E4, SF), (SF, E5, E8), (BF, E5, SF), (HF, E4, E8)])
+def test_block_quant(dev, T, n, rows, dtype, out, scale):
+    g = rng(T * 13 + n)
+    x = rand(g, T, n) * torch.exp2(torch.randint(-20, 20 if dtype != HF else 10, (T, 1), generator=g).float())
+    check_quant(dev, x.to(dtype), rows, out, scale)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("pad", [2, 3, 8])
+@pytest.mark.parametrize("rows", [1, 128])
+def test_block_quant_strides_and_axes(dev, rows, pad):
+    g = rng(pad)
+    check_quant(dev, rand(g, 40, 333, dtype=BF), rows, E4, E8, pad)
+    check_quant(dev, rand(g, 150, 333), rows, E5, SF, pad)
+    if rows == 128:  # matrices: each with blocks of its own
+        check_quant(dev, rand(g, 3, 130, 200, dtype=HF), rows, E4, SF)
+        big = rand(g, 5, 140, 260).to(dev)
+        x = big[::2, 3:133, 5:205]
+        q, s = fw.block_quant(x, block_rows=128)
+        want_q, want_s = quant64(x.cpu(), 128, E4, E8)
+        same(q, want_q, "codes")
+        same(s, want_s, "scales")
+    else:
+        x = rand(g, 2, 3, 200, dtype=BF).to(dev)
+        q, s = fw.block_quant(x)
+        q2, s2 = fw.block_quant(x.view(6, 200))
+        assert q.shape == (2, 3, 200) and s.shape == (2, 3, 2)
+        assert torch.equal(q.view(torch.uint8).view(6, 200), q2.view(torch.uint8))
+        assert torch.equal(s.view(torch.uint8).view(6, 2), s2.view(torch.uint8))
+        q, s = fw.block_quant(x[0, 0])
+        assert q.shape == (200,) and s.shape == (2,)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [1, 128])
+@pytest.mark.parametrize("out", [E4, E5])
+@pytest.mark.parametrize("scale", [SF, E8])
+def test_block_quant_special_blocks(dev, rows, out, scale):
+    """Zeros, infinities, NaN, the largest and the smallest values: each block by itself."""
+    x = rand(rng(1), 256, 128 * 9 + 40)
+    for i, v in enumerate((0.0, INF, -INF, math.nan, 3.4028234e38, 2.0 ** -149, 2.0 ** -126, 1e-40)):
+        if i in (1, 2, 3):
+            x[5, 128 * i + 77] = v
+            x[200, 128 * i] = v
+        else:
+            x[:, 128 * i:128 * i + 128] = v
+    x[:, 128 * 8:] = 0
+    x[7, -1] = -INF  # in the last, shorter block
+    check_quant(dev, x, rows, out, scale)
+    for m in (MOST[out], 2 * MOST[out], MOST[out] * (1 + 2.0 ** -23), MOST[out] * (1 - 2.0 ** -24), 1.75, 1.0, 2.0 ** 100):
+        y = x[:, :256].abs().nan_to_num().clamp(0, 1) * 0.3 * m
+        y[::128, ::128] = m
+        check_quant(dev, y[:128, :128].contiguous(), rows, out, scale)
+    check_quant(dev, torch.zeros(3, 200, dtype=BF), rows, out, scale)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [1, 128])
+@pytest.mark.parametrize("out", [E4, E5])
+def test_block_quant_codes_are_the_nearest(dev, rows, out):
+    """Values on and next to the borders between two codes under scales that
+    are no powers of two: the code is that of the whole quotient."""
+    values = torch.arange(1, 256, dtype=torch.uint8).view(out).to(f64)
+    values = values[values.isfinite() & (values > 0)].sort().values
+    border = (values[1:] + values[:-1]) / 2
+    x = torch.zeros(128, 128, dtype=f64)
+    for i in range(128):
+        m = (1 + i / 130.0) * MOST[out] * 0.37
+        s = float((torch.tensor(m).float() / MOST[out]).to(f64)) if rows == 1 else None
+        x[i, 1:] = border[(torch.arange(127) * 7 + i * 11) % len(border)] * (s or 1.0)
+        x[i, 0] = m if rows == 1 else 0
+    if rows == 128:
+        m = torch.tensor(1.23 * MOST[out]).float()
+        x *= float((m / MOST[out]).to(f64))
+        x[0, 0] = m.to(f64)
+    x = x.float()
+    x[:, 1:] = (x[:, 1:].contiguous().view(torch.int32) + torch.randint(-2, 3, (128, 127), generator=rng(2)).int()).view(SF)
+    check_quant(dev, x, rows, out, SF)
+
+
+@pytest.mark.gpu
+def test_block_quant_empty(dev):
+    for shape in ((0, 128), (4, 0), (0, 0)):
+        for rows in (1, 128):
+            q, s = fw.block_quant(torch.empty(shape, device=dev), block_rows=rows)
+            assert q.shape == shape and s.shape == (shape[0] if rows == 1 else blocks(shape[0]), blocks(shape[1]))
+    q, s = fw.block_quant(torch.empty(0, 5, 128, device=dev), block_rows=128)
+    assert q.shape == (0, 5, 128) and s.shape == (0, 1, 1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,n,rows,dtype,scale", [(14001, 8057, 1, BF, E8), (9001, 8071, 128, SF, SF)])
+def test_block_quant_past_the_cache(dev, T, n, rows, dtype, scale):
+    """More than 192 MiB: passes by the last-level cache.  Compared on the GPU, a slice at a time."""
+    note(f"block codes past the cache {T}x{n}")
+    x = torch.randn(T, n, device=dev, generator=torch.Generator(device=dev).manual_seed(3)).to(dtype)
+    q, s = fw.block_quant(x, block_rows=rows, scale_dtype=scale)
+    for r in range(0, T, 2048):
+        want_q, want_s = quant64(x[r:r + 2048], rows, E4, scale)
+        assert torch.equal(q[r:r + 2048].float().to(f64), want_q)
+        assert torch.equal(s[r // rows:(r + 2048) // rows].float().to(f64)[:len(want_s)], want_s)
+
+
+# ---- the gated activation -----------------------------------------------------
+def silu64(a):
+    return a * torch.sigmoid(a)
+
+
+def check_codes_of(q, s, v, out, scale, what):
+    """Codes and scales of computed values, which are off by F of themselves."""
+    T, n = v.shape
+    m = torch.nn.functional.pad(v.abs(), (0, -n % 128)).unflatten(-1, (-1, 128)).amax(-1)
+    s64 = s.cpu().float().to(f64)
+    lo, hi = (scale64((m * k).float().to(f64), out, scale) for k in (1 - F, 1 + F))
+    if scale == SF:
+        assert bool(((s64 >= lo * (1 - F)) & (s64 <= hi * (1 + F))).all()), what + ": scales"
+    else:
+        assert bool(((s64 == lo) | (s64 == hi)).all()), what + ": scales"
+    at = spread(s64, T, n, 1)
+    z = (v / at).clamp(-MOST[out], MOST[out])
+    close(q.float(), z, half_step(z, out) + z.abs() * F, what)
+
+
+def check_swiglu(dev, T, n, dtype, out, scale, keep, place="halves", pad=0):
+    g = rng(T * 7 + n)
+    gate, up = rand(g, T, n, std=3.0, dtype=dtype), rand(g, T, n, dtype=dtype)
+    note(f"swiglu {T}x{n} {dtype} {out} {scale} keep={keep} {place} pad={pad}")
+    if place == "halves":
+        both = wide(torch.cat([gate, up], 1), pad, dev)
+        a, b = both[:, :n], both[:, n:]
+    else:
+        a, b = wide(gate, pad, dev), up.to(dev)
+    r = fw.swiglu_block_quant(a, b, out_dtype=out, scale_dtype=scale, keep=keep)
+    torch.cuda.synchronize(dev)
+    assert r.codes.shape == (T, n) and r.scale.shape == (T, blocks(n)) and r.codes.dtype == out and r.scale.dtype == scale
+    check_codes_of(r.codes, r.scale, silu64(gate.to(f64)) * up.to(f64), out, scale, "codes")
+    if not keep:
+        assert r.kept is None and r.kept_scale is None
+        return
+    assert r.kept.shape == (T, 2 * n) and r.kept_scale.shape == (T, 2 * blocks(n))
+    for i, v in enumerate((gate, up)):
+        want_q, want_s = quant64(v, 1, out, scale)
+        same(r.kept[:, i * n:i * n + n], want_q, "kept codes")
+        same(r.kept_scale[:, i * blocks(n):(i + 1) * blocks(n)], want_s, "kept scales")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,n", [(1, 1), (1, 128), (3, 129), (5, 7), (33, 1925), (300, 1000), (64, 4096)])
+@pytest.mark.parametrize("dtype,out,scale,keep", [(BF, E4, E8, True), (HF, E5, SF, False), (SF, E4, SF, True), (SF, E5, E8, False)])
+def test_swiglu(dev, T, n, dtype, out, scale, keep):
+    check_swiglu(dev, T, n, dtype, out, scale, keep)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("pad", [2, 3, 8])
+def test_swiglu_strides(dev, pad):
+    check_swiglu(dev, 40, 333, BF, E4, E8, True, "halves", pad)
+    check_swiglu(dev, 40, 333, SF, E5, SF, True, "apart", pad)
+
+
+@pytest.mark.gpu
+def test_swiglu_special_values(dev):
+    """Gates far out, where exp overflows or vanishes, and blocks with an infinity or a NaN."""
+    gate = torch.tensor([0.0, -0.0, 1e-30, 50, 88, 89, 100, 1e4, 1e30, -50, -87, -88, -89, -100, -1e4, -1e30]).repeat(8)
+    gate = gate.expand(5, 128).contiguous()
+    up = torch.ones(5, 128)
+    up[1] = 0.0
+    gate[2, 3], up[3, 5], gate[4, 7] = math.nan, INF, -INF
+    r = fw.swiglu_block_quant(gate.to(dev), up.to(dev), keep=True)
+    s, q = r.scale.cpu().float(), r.codes.cpu().float()
+    h = silu64(gate[:2].to(f64)) * up[:2].to(f64)
+    want_q, want_s = quant64(h.float(), 1, E4, E8)
+    same(q[:2], want_q, "codes")
+    same(s[:2], want_s, "scales")
+    assert s[2:].isnan().all() and q[2:].isnan().all()
+    ks = r.kept_scale.cpu().float()
+    assert ks[2, 0].isnan() and ks[3, 1].isnan() and ks[4, 0].isnan() and not ks[:, 0][[0, 1, 3]].isnan().any()
+
+
+def swiglu_grad64(g, a, b):
+    p, q = torch.sigmoid(a), torch.sigmoid(-a)
+    return torch.cat([g * b * p * (1 + a * q), g * a * p], 1)
+
+
+def kept_values(kept, s, n):
+    v = kept.cpu().float().to(f64)
+    s = s.cpu().float().to(f64)
+    k = blocks(n)
+    return [v[:, i * n:i * n + n] * spread(s[:, i * k:(i + 1) * k], len(v), n, 1) for i in (0, 1)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,n", [(1, 1), (1, 128), (3, 129), (5, 7), (33, 1925), (300, 1000), (64, 4096)])
+@pytest.mark.parametrize("dtype,out,scale", [(BF, E4, E8), (HF, E5, SF), (SF, E4, SF), (SF, E5, E8)])
+def test_swiglu_grad(dev, T, n, dtype, out, scale):
+    gen = rng(T + n)
+    gate, up, g = rand(gen, T, n, std=3.0, dtype=dtype), rand(gen, T, n, dtype=dtype), rand(gen, T, n, std=0.1, dtype=dtype)
+    r = fw.swiglu_block_quant(gate.to(dev), up.to(dev), out_dtype=out, scale_dtype=scale, keep=True)
+    for pad in (0, 3):
+        note(f"swiglu gradient {T}x{n} {dtype} {out} {scale} pad={pad}")
+        d = fw.swiglu_block_backward(wide(g, pad, dev), r.kept, r.kept_scale)
+        torch.cuda.synchronize(dev)
+        assert d.shape == (T, 2 * n) and d.dtype == dtype
+        a, b = kept_values(r.kept, r.kept_scale, n)
+        want = swiglu_grad64(g.to(f64), a, b)
+        # 1 + a (1 - p) adds two terms
+        size = torch.cat([(g.to(f64) * b * torch.sigmoid(a)).abs() * (1 + (a * torch.sigmoid(-a)).abs()), want[:, n:].abs()], 1)
+        close(d, want, half_step(want, dtype) + size * F, "gradient")
+
+
+@pytest.mark.gpu
+def test_swiglu_grad_against_differences(dev):
+    gen = rng(4)
+    r = fw.swiglu_block_quant(rand(gen, 6, 300, std=2.0).to(dev), rand(gen, 6, 300).to(dev), scale_dtype=SF, keep=True)
+    g = rand(gen, 6, 300)
+    d = fw.swiglu_block_backward(g.to(dev), r.kept, r.kept_scale).cpu().to(f64)
+    a, b = kept_values(r.kept, r.kept_scale, 300)
+    f = lambda a, b: float((g.to(f64) * silu64(a) * b).sum())  # noqa: E731
+    step = 1e-5
+    for _ in range(3):
+        da, db = rand(gen, 6, 300).to(f64), rand(gen, 6, 300).to(f64)
+        want = (f(a + step * da, b + step * db) - f(a - step * da, b - step * db)) / (2 * step)
+        got = d * torch.cat([da, db], 1)
+        # the differences' own error: step^2 and 2^-53 / step of the terms
+        assert abs(float(got.sum()) - want) <= F * 2 * float(got.abs().sum()) + 1e-8 * float((g.to(f64) * silu64(a) * b).abs().sum())
+
+
+@pytest.mark.gpu
+def test_swiglu_grad_special_values(dev):
+    """Far gates give 0 or the gradient of up alone; a block kept as NaN gives NaN, and nothing else does."""
+    gate = torch.tensor([0.0, 300.0, 1e4, 1e30, -300.0, -1e4, -1e30, 5.0]).repeat(16)[None].repeat(3, 1)
+    gate = (gate * torch.tensor([1.0, 1.0, -1.0])[:, None])
+    up = torch.ones(3, 128)
+    up[1, 0] = math.nan
+    r = fw.swiglu_block_quant(gate.to(dev), up.to(dev), scale_dtype=SF, out_dtype=E5, keep=True)
+    d = fw.swiglu_block_backward(torch.ones(3, 128, device=dev), r.kept, r.kept_scale).cpu()
+    a, b = kept_values(r.kept, r.kept_scale, 128)
+    want = swiglu_grad64(torch.ones(3, 128, dtype=f64), a, b)
+    assert d[1, :128].isnan().all() and not d[1, 128:].isnan().any() and not d[0].isnan().any() and not d[2].isnan().any()
+    close(d, want, want.abs().nan_to_num() * F + 1e-30, "gradient")
+
+
+@pytest.mark.gpu
+def test_swiglu_empty(dev):
+    z = torch.empty(0, 64, device=dev)
+    r = fw.swiglu_block_quant(z, z, keep=True)
+    assert r.codes.shape == (0, 64) and r.kept.shape == (0, 128) and r.kept_scale.shape == (0, 2)
+    assert fw.swiglu_block_backward(z, r.kept, r.kept_scale).shape == (0, 128)
+    z = torch.empty(3, 0, device=dev)
+    r = fw.swiglu_block_quant(z, z, keep=True)
+    assert r.codes.shape == (3, 0) and fw.swiglu_block_backward(z, r.kept, r.kept_scale).shape == (3, 0)
+
+
+# ---- refusals (no GPU) ---------------------------------------------------------
+def c_quant(**kw):
+    a = dict(x=16, xd=0, ldx=64, xs=0, E=1, T=2, n=64, rows=1, q=16, qd=3, s=16, sd=1)
+    a.update(kw)
+    return block_operators._lib().emu_block_quant(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(E=-1), 1), (dict(T=-1), 1), (dict(n=-1), 1), (dict(xd=3), 1), (dict(xd=9), 1), (dict(qd=5), 1), (dict(qd=0), 1),
+    (dict(sd=2), 1), (dict(sd=-1), 1), (dict(rows=0), 1), (dict(rows=64), 1), (dict(x=None), 1), (dict(q=None), 1),
+    (dict(s=None), 1), (dict(ldx=63), 1), (dict(x=17), 1), (dict(s=18, sd=0), 1), (dict(E=2, xs=-1), 1), (dict(T=2 ** 31), 3),
+    (dict(n=2 ** 30 + 1, ldx=2 ** 31), 3), (dict(ldx=2 ** 61), 1), (dict(E=0), 0), (dict(T=0), 0), (dict(n=0), 0)])
+def test_block_quant_refusals(kw, status):
+    assert c_quant(**kw) == status
+    assert bool(block_operators._lib().emu_last_error_message()) == (status != 0)
+
+
+def c_swiglu(**kw):
+    a = dict(g=16, ldg=64, u=16, ldu=64, d=0, T=2, F=64, q=16, qd=3, s=16, sd=1, k=None, ks=None)
+    a.update(kw)
+    return block_operators._lib().emu_swiglu_block_quant(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(T=-1), 1), (dict(F=-1), 1), (dict(d=3), 1), (dict(qd=5), 1), (dict(sd=2), 1), (dict(g=None), 1), (dict(u=None), 1),
+    (dict(q=None), 1), (dict(s=None), 1), (dict(ldg=63), 1), (dict(ldu=63), 1), (dict(k=16), 1), (dict(ks=16), 1), (dict(g=17), 1),
+    (dict(u=17), 1), (dict(s=18, sd=0), 1), (dict(k=16, ks=18, sd=0), 1), (dict(T=2 ** 31), 3), (dict(T=0), 0), (dict(F=0), 0)])
+def test_swiglu_refusals(kw, status):
+    assert c_swiglu(**kw) == status
+
+
+def c_swiglu_grad(**kw):
+    a = dict(g=16, gd=0, ldg=64, k=16, kd=3, s=16, sd=1, T=2, F=64, out=16, ldo=128)
+    a.update(kw)
+    return block_operators._lib().emu_swiglu_block_backward(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(T=-1), 1), (dict(F=-1), 1), (dict(gd=3), 1), (dict(kd=5), 1), (dict(sd=2), 1), (dict(g=None), 1), (dict(k=None), 1),
+    (dict(s=None), 1), (dict(out=None), 1), (dict(ldg=63), 1), (dict(ldo=127), 1), (dict(g=17), 1), (dict(out=17), 1),
+    (dict(s=18, sd=0), 1), (dict(T=2 ** 31), 3), (dict(T=0), 0), (dict(F=0), 0)])
+def test_swiglu_grad_refusals(kw, status):
+    assert c_swiglu_grad(**kw) == status
+
+
+def test_host_tensors_are_refused():
+    x = torch.zeros(2, 128)
+    with pytest.raises(ValueError):
+        fw.block_quant(x)
+    with pytest.raises(ValueError):
+        fw.swiglu_block_quant(x, x)
+    with pytest.raises(ValueError):
+        fw.swiglu_block_backward(x, x.to(E4), x)
+
+
+@pytest.mark.gpu
+def test_quant_binding_refusals(dev):
+    x = torch.zeros(4, 256, device=dev)
+    q, s = fw.block_quant(x)
+    for bad in (lambda: fw.block_quant(x.t()), lambda: fw.block_quant(x, block_rows=64), lambda: fw.block_quant(x[None, None], 128),
+                lambda: fw.block_quant(x[0], 128), lambda: fw.swiglu_block_quant(x, x[:2]), lambda: fw.swiglu_block_quant(x, x.cpu()),
+                lambda: fw.swiglu_block_backward(x, q, s), lambda: fw.swiglu_block_backward(x[:, :128], q, s[:1]),
+                lambda: fw.swiglu_block_backward(x[:, :128], q.t().contiguous().t(), s)):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: fw.block_quant(x.double()), lambda: fw.swiglu_block_quant(x, x.bfloat16()), lambda: fw.block_quant(x, "1"),
+                lambda: fw.swiglu_block_backward(x[:, :128], x, s), lambda: fw.swiglu_block_backward(x[:, :128], q, s.view(torch.uint8))):
+        with pytest.raises(TypeError):
+            bad()
+    for bad in (lambda: fw.block_quant(x, out_dtype=I8), lambda: fw.block_quant(x, scale_dtype=BF),
+                lambda: fw.swiglu_block_quant(x, x, out_dtype=SF)):
+        with pytest.raises(fw.EmuError):
+            bad()
+    y = x.clone().requires_grad_()
+    for bad in (lambda: fw.block_quant(y), lambda: fw.swiglu_block_quant(x, y), lambda: fw.swiglu_block_backward(y[:, :128], q, s)):
+        with pytest.raises(RuntimeError):
+            bad()
