@@ -32,6 +32,10 @@ FLAGS = [
     f"-I{os.path.join(ROOT, 'include')}",
 ]
 
+# The accumulators of tiles stay in ordinary registers: the compiler otherwise
+# copies them to and fro in the loop.
+MFMA_FLAGS = ["-mllvm", "-amdgpu-mfma-vgpr-form=true"]
+
 # (block width, x format, w format): e5m2 x e5m2 is rejected by the ABI.
 VARIANTS = [(b, xf, wf) for b in (32, 16) for xf, wf in ((0, 0), (0, 1), (1, 0))]
 
@@ -41,11 +45,13 @@ def _units(objdir: str):
              (os.path.join(CSRC, "emu_specials.hip"), os.path.join(objdir, "emu_specials.o"), []),
              (os.path.join(CSRC, "emu_noalloc.hip"), os.path.join(objdir, "emu_noalloc.o"), []),
              (os.path.join(CSRC, "emu_api.cpp"), os.path.join(objdir, "emu_api.o"), [])]
-    for name in ("emu_norm.hip", "emu_int8.hip", "emu_logprobs.hip", "ops_api.cpp", "emu_block_quant.hip", "ops_block_api.cpp"):
-        # the accumulators of the int8 tiles stay in ordinary registers: the
-        # compiler otherwise copies them to and fro in the loop
-        extra = ["-mllvm", "-amdgpu-mfma-vgpr-form=true"] if name == "emu_int8.hip" else []
+    for name in ("emu_norm.hip", "emu_int8.hip", "emu_logprobs.hip", "ops_api.cpp", "emu_block_quant.hip",
+                 "emu_block_plan.hip", "ops_block_api.cpp"):
+        extra = MFMA_FLAGS if name == "emu_int8.hip" else []
         units.append((os.path.join(CSRC, name), os.path.join(objdir, name.split(".")[0] + ".o"), extra))
+    for af, wf in ((0, 0), (0, 1), (1, 0), (1, 1)):
+        defs = [*MFMA_FLAGS, f"-DEMU_BLOCK_AF={af}", f"-DEMU_BLOCK_WF={wf}"]
+        units.append((os.path.join(CSRC, "emu_block_mm.hip"), os.path.join(objdir, f"emu_block_mm_{af}{wf}.o"), defs))
     for b, xf, wf in VARIANTS:
         defs = [f"-DEMU_VARIANT_BLK={b}", f"-DEMU_VARIANT_XF={xf}", f"-DEMU_VARIANT_WF={wf}"]
         units.append((os.path.join(CSRC, "emu_variant.hip"), os.path.join(objdir, f"emu_variant_{b}_{xf}{wf}.o"), defs))

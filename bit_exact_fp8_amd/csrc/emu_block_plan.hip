@@ -1,0 +1,238 @@
+// emu_block_plan.hip -- emu_block_scaled_mm and its form by groups of rows:
+// which kernel of emu_block_mm.hip runs, operands laid out anew where their
+// rows are not aligned to 16 bytes, and the sums of a split K.
+#include <hip/hip_runtime.h>
+
+#include "ops_block.h"
+#include "ops_tiles.h"
+
+namespace emu {
+
+extern template void launch_block_kernel<0, 0>(const BlockMMParams &, const BlockPlan &, float *, hipStream_t);
+extern template void launch_block_kernel<0, 1>(const BlockMMParams &, const BlockPlan &, float *, hipStream_t);
+extern template void launch_block_kernel<1, 0>(const BlockMMParams &, const BlockPlan &, float *, hipStream_t);
+extern template void launch_block_kernel<1, 1>(const BlockMMParams &, const BlockPlan &, float *, hipStream_t);
+
+namespace {
+
+// Rows of E matrices laid out anew, with the leading dimension `ldo`, a
+// multiple of 128, and zeros past K.  A workgroup takes `rows` of them, the
+// first from row0 on.
+template <bool WORDS>
+__global__ __launch_bounds__(256) void block_repack(const int8_t *in, int64_t ld, int64_t stride, int64_t per, int64_t total,
+                                                    int64_t K, int8_t *out, int64_t ldo, int64_t row0, int rows)
+{
+    const int chunks = (int)(ldo / 16);
+    const int64_t first = row0 + (int64_t)blockIdx.x * rows;
+    for (int i = threadIdx.x; i < rows * chunks; i += 256) {
+        const int64_t row = first + i / chunks, k = i % chunks * 16;
+        if (row >= total) return;
+        *reinterpret_cast<i32x4 *>(out + row * ldo + k) = load16<WORDS>(in + row / per * stride + row % per * ld, k, K);
+    }
+}
+
+// The sums of S splits and the epilogue, four outputs a thread.
+__global__ __launch_bounds__(256) void block_join(BlockMMParams p, const float *part, int S)
+{
+    const int64_t quads = (p.N + 3) / 4, id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t m = id / quads, n = id % quads * 4;
+    if (m >= p.M) return;
+    f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+    typedef f32x4 words __attribute__((aligned(4)));
+    const float *at = part + m * p.N + n;
+    for (int s = 0; s < S; ++s, at += p.M * p.N) {
+        if (n + 4 <= p.N) {
+            sum += *reinterpret_cast<const words *>(at);
+        } else {
+            for (int e = 0; e < 4; ++e)
+                if (n + e < p.N) sum[e] += at[e];
+        }
+    }
+    with_type(p.out_dtype, [&](auto *type) {
+        typedef std::remove_pointer_t<decltype(type)> E;
+        if (p.bias) {
+            for (int e = 0; e < 4; ++e) {
+                const int64_t c = n + e < p.N ? n + e : p.N - 1;
+                sum[e] += p.bias_f32 ? static_cast<const float *>(p.bias)[c] : (float)static_cast<const E *>(p.bias)[c];
+            }
+        }
+        store_valid(static_cast<E *>(p.out) + m * p.ldo + n, __builtin_convertvector(sum, Four<E>), p.N - n);
+    });
+}
+
+// The tiles, with what one stage of a tile costs a CU in microseconds in each mode.
+struct Tile {
+    int bm, bn;
+    double stage[3];
+};
+constexpr Tile kTiles[] = {{64, 64, {0.20, 0.20, 0.25}}, {128, 128, {0.55, 0.55, 0.75}}, {256, 256, {1.60, 1.70, 0}}};
+
+struct Plan {
+    BlockPlan kernel;
+    bool repack_a, repack_w;
+    int64_t ld;                  // of repacked operands
+    int64_t a_bytes, w_bytes, part_bytes;
+};
+
+bool needs_repack(int64_t K, bool aligned) { return K > 0 && (!aligned || K % 16 != 0); }
+
+int64_t mean_rows(int64_t M, int E, bool grouped) { return grouped && E > 0 ? ceil_div(M, E) : M; }
+
+Plan make_plan(int64_t M, int64_t N, int64_t K, int E, bool grouped, int mode, bool a_aligned, bool w_aligned)
+{
+    Plan p{};
+    BlockPlan &k = p.kernel;
+    k.mode = mode;
+    k.S = 1;
+    k.tile = -1;
+    const int64_t total = blocks_of(K);
+    k.stages = total ? (int)total : 1;
+    const bool ra = needs_repack(K, a_aligned), rw = needs_repack(K, w_aligned);
+    // Few rows (of each group, in the mean) read w once and wait for nothing.
+    const int64_t mean = mean_rows(M, E, grouped);
+    if (mean <= 32 || (mean <= 64 && (ra || rw)) || K == 0) {
+        k.rows = mean <= 16 || K == 0 ? 1 : mean <= 32 ? 2 : 4;
+        k.waves = k.rows == 4 ? 8 : K > 4096 ? (k.rows == 1 ? 16 : 8) : 4;
+        return p;
+    }
+    p.repack_a = ra;
+    p.repack_w = rw;
+    p.ld = total * kStage;
+    p.a_bytes = ra ? M * p.ld : 0;
+    p.w_bytes = rw ? (int64_t)E * N * p.ld : 0;
+    // The fastest estimate: 1 us and its stages for each round of 256 tiles
+    // (one for a CU), and for a split of K 5 us and its sums at 4 TB/s, there
+    // and back.  Each group's last tile is half full in the mean.
+    double best = 0.0;
+    for (int i = 0; i < (mode == kExact ? 2 : 3); ++i)
+        for (int S = 1; S <= (grouped ? 1 : 8); S *= 2) {
+            const int64_t stages = ceil_div(total, S);
+            if (S > 1 && stages < 4) break;
+            const int64_t tm = grouped ? M / kTiles[i].bm + (E < M ? E : M) / 2 + 1 : ceil_div(M, kTiles[i].bm);
+            const int64_t tiles = tm * ceil_div(N, kTiles[i].bn);
+            const double rounds = (double)ceil_div(tiles * S, 256);
+            double us = rounds * (1.0 + (double)stages * kTiles[i].stage[mode]);
+            if (S > 1) us += 5.0 + (double)S * (double)M * (double)N * 8.0 / 4e6;
+            if (k.tile >= 0 && us >= best) continue;
+            best = us;
+            k.tile = i;
+            k.S = S;
+        }
+    k.stages = total ? (int)ceil_div(total, k.S) : 1;
+    k.S = total ? (int)ceil_div(total, k.stages) : 1;
+    p.part_bytes = k.S > 1 ? k.S * M * N * 4 : 0;
+    return p;
+}
+
+int mode_of(bool fp32_out, bool e8m0) { return fp32_out ? kExact : e8m0 ? kHardware : kScaled; }
+
+// A launch's rows (dense) and columns, so that its grid stays below 2^32
+// threads: of groups, whose rows one launch has to hold, fewer columns at a time.
+constexpr int64_t kSliceM = 1 << 18, kSliceN = 1 << 17;
+int64_t slice_n(int64_t M, int64_t K, int E, bool grouped)
+{
+    if (!grouped) return kSliceN;
+    // at most 2^21 workgroups, of the few rows' kernel or of the smallest tile
+    const int64_t unit = mean_rows(M, E, grouped) <= 64 || K == 0 ? 16 : 64;
+    const int64_t n = (int64_t(1) << 21) / (ceil_div(M, unit) + E + 1) * unit / kBlock * kBlock;
+    return n < kBlock ? kBlock : n > kSliceN ? kSliceN : n;
+}
+
+bool in_words(const BlockMMParams &p)
+{
+    return ((reinterpret_cast<uintptr_t>(p.a) | reinterpret_cast<uintptr_t>(p.w) | p.lda | p.ldw | p.w_stride) & 3) == 0;
+}
+
+// `out`: 16-byte aligned
+void repack(const int8_t *in, int64_t ld, int64_t stride, int64_t per, int64_t total, int64_t K, int8_t *out, int64_t ldo,
+            hipStream_t stream)
+{
+    const int rows = (int)ceil_div(512, ldo / 16);  // some two chunks a thread
+    constexpr int64_t most = int64_t(1) << 22;      // workgroups of a launch
+    for (int64_t r = 0; r < total; r += most * rows) {
+        const int64_t left = ceil_div(total - r, rows);
+        const dim3 grid((unsigned)(left < most ? left : most));
+        if (((reinterpret_cast<uintptr_t>(in) | ld | stride) & 3) == 0)
+            hipLaunchKernelGGL((block_repack<true>), grid, dim3(256), 0, stream, in, ld, stride, per, total, K, out, ldo, r, rows);
+        else
+            hipLaunchKernelGGL((block_repack<false>), grid, dim3(256), 0, stream, in, ld, stride, per, total, K, out, ldo, r, rows);
+    }
+}
+
+void launch_slice(int a_dtype, int w_dtype, BlockMMParams p, bool a_aligned, bool w_aligned, hipStream_t stream)
+{
+    const dim3 quads((unsigned)ceil_div(p.M * ceil_div(p.N, 4), 256));
+    if (p.K == 0 && !p.ends) {
+        hipLaunchKernelGGL(block_join, quads, dim3(256), 0, stream, p, nullptr, 0);
+        return;
+    }
+    const Plan plan = make_plan(p.M, p.N, p.K, p.E, p.ends != nullptr, mode_of(p.out_dtype == EMU_DT_FP32, p.e8m0), a_aligned, w_aligned);
+    BlockPlan k = plan.kernel;
+    k.words = in_words(p);
+    char *ws = static_cast<char *>(p.ws);
+    if (plan.repack_a) {
+        repack(p.a, p.lda, 0, p.M, p.M, p.K, reinterpret_cast<int8_t *>(ws), plan.ld, stream);
+        p.a = reinterpret_cast<const int8_t *>(ws);
+        p.lda = plan.ld;
+    }
+    if (plan.repack_w) {
+        int8_t *w = reinterpret_cast<int8_t *>(ws + plan.a_bytes);
+        repack(p.w, p.ldw, p.w_stride, p.N, p.E * p.N, p.K, w, plan.ld, stream);
+        p.w = w;
+        p.ldw = plan.ld;
+        p.w_stride = p.N * plan.ld;
+    }
+    if (plan.repack_a && plan.repack_w) p.K = plan.ld;
+    float *part = k.S > 1 ? reinterpret_cast<float *>(ws + plan.a_bytes + plan.w_bytes) : nullptr;
+    const bool a5 = a_dtype == EMU_DT_E5M2, w5 = w_dtype == EMU_DT_E5M2;
+    (a5 ? w5 ? launch_block_kernel<1, 1> : launch_block_kernel<1, 0> : w5 ? launch_block_kernel<0, 1> : launch_block_kernel<0, 0>)(
+        p, k, part, stream);
+    if (part)
+        hipLaunchKernelGGL(block_join, quads, dim3(256), 0, stream, p, part, k.S);
+}
+
+}  // namespace
+
+int64_t block_mm_workspace(int64_t M, int64_t N, int64_t K, int E, bool grouped, bool fp32_out, bool a_aligned, bool w_aligned)
+{
+    if (K == 0) return 0;
+    int64_t most = 0;
+    const int64_t step = slice_n(M, K, E, grouped), slice_m = grouped ? M : kSliceM;
+    for (int64_t m : {M < slice_m ? M : slice_m, M % slice_m})
+        for (int64_t n : {N < step ? N : step, N % step}) {
+            if (!m || !n) continue;
+            for (bool e8m0 : {false, true}) {
+                const Plan p = make_plan(m, n, K, E, grouped, mode_of(fp32_out, e8m0), a_aligned, w_aligned);
+                const int64_t need = p.a_bytes + p.w_bytes + p.part_bytes;
+                if (need > most) most = need;
+            }
+        }
+    return most;
+}
+
+hipError_t launch_block_mm(int a_dtype, int w_dtype, const BlockMMParams &p, bool a_aligned, bool w_aligned, hipStream_t stream)
+{
+    const int64_t size = p.out_dtype == EMU_DT_FP32 ? 4 : 2, unit = p.e8m0 ? 1 : 4;
+    const bool grouped = p.ends != nullptr;
+    const int64_t step = slice_n(p.M, p.K, p.E, grouped), slice_m = grouped ? p.M : kSliceM;
+    for (int64_t m = 0; m < p.M; m += slice_m)
+        for (int64_t n = 0; n < p.N; n += step) {
+            BlockMMParams q = p;
+            q.M = p.M - m < slice_m ? p.M - m : slice_m;
+            q.N = p.N - n < step ? p.N - n : step;
+            if (p.K) {
+                q.a = p.a + m * p.lda;
+                q.w = p.w + n * p.ldw;
+                q.sa = static_cast<const char *>(p.sa) + m * p.sa_row * unit;
+                q.sw = static_cast<const char *>(p.sw) + n / kBlock * p.sw_row * unit;
+            }
+            if (p.bias) q.bias = static_cast<const char *>(p.bias) + n * (p.bias_f32 ? 4 : size);
+            q.out = static_cast<char *>(p.out) + (m * p.ldo + n) * size;
+            launch_slice(a_dtype, w_dtype, q, a_aligned, w_aligned, stream);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
+    return hipSuccess;
+}
+
+}  // namespace emu

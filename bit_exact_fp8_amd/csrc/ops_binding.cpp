@@ -534,6 +534,15 @@ bool truth(PyObject *o)
     return b != 0;
 }
 
+// Each group's end in rows: their bits.
+int ends_bits(const Tensor &ends, int64_t E, c10::Device device)
+{
+    if (ends.scalar_type() != ScalarType::Int && ends.scalar_type() != ScalarType::Long)
+        type_error("ends must be int32 or int64, not " + str(ends.scalar_type()));
+    dense("ends", ends, {E}, device);
+    return ends.scalar_type() == ScalarType::Int ? 32 : 64;
+}
+
 // x, block_rows, out_dtype, scale_dtype
 PyObject *block_quant(PyObject *const *a)
 {
@@ -618,6 +627,126 @@ PyObject *swiglu_block_backward(PyObject *const *a)
     return wrap(grad);
 }
 
+// Codes, their scales, and where both lie: rows (of one matrix) by K.
+struct Coded {
+    int8_t *p;
+    int64_t rows, K, ld, stride;
+    void *scales;
+    int64_t s_row, s_block, s_stride;
+    bool aligned() const
+    {
+        return !((reinterpret_cast<uintptr_t>(p) | ld | stride) & 15) && ld <= EMU_BLOCK_MAX_ALIGNED_LD;
+    }
+};
+// mat1 [M, K] with scale_a [M, blocks of K]
+Coded left(const Tensor &x, const Tensor &s)
+{
+    codes("mat1", x);
+    scales("scale_a", s);
+    if (x.dim() != 2) value_error("mat1 must be 2-D");
+    if (!x.is_cuda()) value_error("the operands must be CUDA tensors, not " + x.device().str());
+    const int64_t M = x.size(0), K = x.size(1);
+    if (K > 1 && M > 0 && x.stride(1) != 1) value_error("mat1 must be row-major [M, K] (unit stride along K)");
+    shaped("scale_a", s, {M, blocks_of(K)}, x.device());
+    return {as<int8_t>(x), M, K, M > 1 && K > 0 ? x.stride(0) : K, 0, ptr(s), M > 1 ? s.stride(0) : 0,
+            K > EMU_BLOCK ? s.stride(1) : 0, 0};
+}
+// mat2 [K, N] (or [E, K, N]) column-major, with scale_b [blocks of K, blocks of N] (or [E, ...])
+Coded right(const Tensor &w, const Tensor &s, const Tensor &x, int64_t K, bool grouped)
+{
+    codes("mat2", w);
+    scales("scale_b", s);
+    const int64_t d = grouped ? 1 : 0;
+    if (w.dim() != 2 + d) value_error(grouped ? "mat2 must be 3-D" : "mat2 must be 2-D");
+    on_device("mat2", w, x.device());
+    const int64_t N = w.size(1 + d), E = grouped ? w.size(0) : 1;
+    if (w.size(d) != K) value_error("inner dimensions differ: " + std::to_string(K) + " vs " + std::to_string(w.size(d)));
+    if (K > 1 && N > 0 && E > 0 && w.stride(d) != 1) value_error("mat2 must be column-major [K, N] (pass w.t() for a row-major w)");
+    if (grouped)
+        shaped("scale_b", s, {E, blocks_of(K), blocks_of(N)}, x.device());
+    else
+        shaped("scale_b", s, {blocks_of(K), blocks_of(N)}, x.device());
+    return {as<int8_t>(w), N, K, N > 1 && K > 0 ? w.stride(1 + d) : K, E > 1 ? w.stride(0) : 0, ptr(s),
+            N > EMU_BLOCK ? s.stride(1 + d) : 0, K > EMU_BLOCK ? s.stride(d) : 0, E > 1 ? s.stride(0) : 0};
+}
+// An output given, or a new one, of [M, N].
+struct Output {
+    Tensor own;
+    void *p;
+    int64_t ld;
+};
+Output output(const Tensor *given, int64_t M, int64_t N, ScalarType dtype, const Tensor &x)
+{
+    Output o{Tensor(), nullptr, N};
+    if (!given) {
+        o.own = empty({M, N}, x, dtype);
+        o.p = ptr(o.own);
+        return o;
+    }
+    on_device("out", *given, x.device());
+    if (given->dim() != 2 || given->size(0) != M || given->size(1) != N || given->scalar_type() != dtype ||
+        (N > 1 && M > 0 && given->stride(1) != 1))
+        value_error("out must be a row-major [M, N] tensor of out_dtype");
+    if (M > 1) o.ld = given->stride(0);
+    o.p = given->data_ptr();
+    return o;
+}
+void one_type(const Tensor &a, const Tensor &b)
+{
+    if (a.scalar_type() != b.scalar_type()) type_error("scale_a and scale_b must be of one type");
+}
+
+// mat1, mat2, scale_a, scale_b, bias, out_dtype, out
+PyObject *block_scaled_mm(PyObject *const *a)
+{
+    outside_autograd({a[0], a[1], a[2], a[3], a[4]}, {a[6]});
+    const Tensor &x = tensor("mat1", a[0]), &w = tensor("mat2", a[1]), &sa = tensor("scale_a", a[2]), &sb = tensor("scale_b", a[3]);
+    const Coded l = left(x, sa), r = right(w, sb, x, l.K, false);
+    one_type(sa, sb);
+    const ScalarType dtype = dtype_of(a[5], is_float);
+    const Tensor *bias = optional("bias", a[4]), *given = optional("out", a[6]);
+    if (bias) {
+        floating("bias", *bias, dtype);
+        vector("bias", *bias, r.rows, x.device());
+    }
+    const Output o = output(given, l.rows, r.rows, dtype, x);
+    const emu_dtype out_code = static_cast<emu_dtype>(code_of(dtype));
+    const size_t bytes = emu_block_scaled_mm_workspace(l.rows, r.rows, l.K, out_code, l.aligned(), r.aligned());
+    const Tensor ws = workspace(bytes, x);
+    launch(x.device(), [&](hipStream_t stream) {
+        return emu_block_scaled_mm(l.p, code(x), l.ld, r.p, code(w), r.ld, l.rows, r.rows, l.K, l.scales, l.s_row, l.s_block,
+                                   r.scales, r.s_row, r.s_block, scale_code(sa.scalar_type()), ptr(bias),
+                                   bias ? code(*bias) : EMU_DT_BF16, o.p, out_code, o.ld, ptr(ws), bytes, stream);
+    });
+    if (given) written(*given);
+    return given ? held(a[6]) : wrap(o.own);
+}
+
+// mat1, mat2, scale_a, scale_b, ends, out_dtype, out
+PyObject *grouped_block_scaled_mm(PyObject *const *a)
+{
+    outside_autograd({a[0], a[1], a[2], a[3]}, {a[6]});
+    const Tensor &x = tensor("mat1", a[0]), &w = tensor("mat2", a[1]), &sa = tensor("scale_a", a[2]), &sb = tensor("scale_b", a[3]),
+                 &ends = tensor("ends", a[4]);
+    const Coded l = left(x, sa), r = right(w, sb, x, l.K, true);
+    one_type(sa, sb);
+    const int64_t E = w.size(0);
+    const int bits = ends_bits(ends, E, x.device());
+    const ScalarType dtype = dtype_of(a[5], is_float);
+    const Tensor *given = optional("out", a[6]);
+    const Output o = output(given, l.rows, r.rows, dtype, x);
+    const emu_dtype out_code = static_cast<emu_dtype>(code_of(dtype));
+    const size_t bytes = emu_grouped_block_scaled_mm_workspace(l.rows, E, r.rows, l.K, out_code, l.aligned(), r.aligned());
+    const Tensor ws = workspace(bytes, x);
+    launch(x.device(), [&](hipStream_t stream) {
+        return emu_grouped_block_scaled_mm(l.p, code(x), l.ld, r.p, code(w), r.ld, r.stride, l.rows, E, r.rows, l.K, l.scales, l.s_row,
+                                           l.s_block, r.scales, r.s_row, r.s_block, r.s_stride, scale_code(sa.scalar_type()),
+                                           ptr(ends), bits, given ? 0 : 1, o.p, out_code, o.ld, ptr(ws), bytes, stream);
+    });
+    if (given) written(*given);
+    return given ? held(a[6]) : wrap(o.own);
+}
+
 template <PyObject *(*call)(PyObject *const *), int N>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t nargs)
 {
@@ -653,6 +782,8 @@ PyMethodDef g_methods[] = {
     {"block_quant", function<block_quant, 4>(), METH_FASTCALL, nullptr},
     {"swiglu_block_quant", function<swiglu_block_quant, 5>(), METH_FASTCALL, nullptr},
     {"swiglu_block_backward", function<swiglu_block_backward, 3>(), METH_FASTCALL, nullptr},
+    {"block_scaled_mm", function<block_scaled_mm, 7>(), METH_FASTCALL, nullptr},
+    {"grouped_block_scaled_mm", function<grouped_block_scaled_mm, 7>(), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_ops", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

@@ -43,6 +43,49 @@ struct SwigluGradParams {
 };
 hipError_t launch_swiglu_grad(int g_dtype, int q_dtype, bool e8m0, const SwigluGradParams &p, hipStream_t stream);
 
+// The product, dense or by groups of rows (ends not null).  Strides are in
+// elements, those of scales between rows (of w: blocks of 128 of them) and
+// between blocks of K.
+struct BlockMMParams {
+    const int8_t *a, *w;
+    int64_t lda, ldw, w_stride;
+    int64_t M, N, K;
+    const void *sa, *sw;
+    int64_t sa_row, sa_block, sw_row, sw_block, sw_stride;
+    int e8m0;
+    const void *bias;
+    int bias_f32;          // the bias is binary32 (else of out's type)
+    void *out;
+    int out_dtype;
+    int64_t ldo;
+    const void *ends;      // of each group's rows, or null
+    int ends64;            // they are int64 (else int32)
+    int E;
+    int zero_rest;         // rows behind the last group's become 0
+    void *ws;
+};
+// Leading dimensions and row strides of scales whose offsets within a tile stay below 2^31.
+constexpr int64_t kMaxTileLd = EMU_BLOCK_MAX_ALIGNED_LD, kMaxScaleLd = int64_t(1) << 20;
+int64_t block_mm_workspace(int64_t M, int64_t N, int64_t K, int E, bool grouped, bool fp32_out, bool a_aligned, bool w_aligned);
+hipError_t launch_block_mm(int a_dtype, int w_dtype, const BlockMMParams &p, bool a_aligned, bool w_aligned, hipStream_t stream);
+
+// The kernels of one pair of codes' types (emu_block_mm.hip).
+enum BlockMode {
+    kHardware,  // e8m0 scales go into the matrix instruction
+    kScaled,    // each block's sum is multiplied by its scales
+    kExact      // the same, the products summed in binary32
+};
+struct BlockPlan {
+    int mode;        // BlockMode
+    int tile;        // of kBlockTiles, or -1: few rows
+    int rows;        // few rows: fragments of 16 of them
+    int waves;       // few rows: waves of a workgroup
+    bool words;      // few rows: the operands' rows are aligned to 4 bytes
+    int S, stages;   // splits of K, stages of each
+};
+template <int AF, int WF>
+void launch_block_kernel(const BlockMMParams &p, const BlockPlan &plan, float *part, hipStream_t stream);
+
 #ifdef __HIPCC__
 
 // The value of a scale byte: 2^(b - 127) (a subnormal number for 0), NaN for 255.

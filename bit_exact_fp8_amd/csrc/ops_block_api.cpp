@@ -30,6 +30,60 @@ bool far(int64_t ld, int64_t count) { return count > 1 && ld > (INT64_MAX / 16) 
 bool bad_ld(int64_t ld, int64_t cols, int64_t rows) { return ld < cols || far(ld, rows); }
 
 constexpr int64_t kMaxRows = INT32_MAX, kMaxCols = int64_t(1) << 30;
+constexpr int64_t kMaxGroupedRows = int64_t(1) << 24, kMaxGroups = 65536;
+
+// What both products ask of their operands; null where all is well.
+struct Operand {
+    const void *p;
+    int64_t ld, stride;
+    bool aligned() const
+    {
+        return aligned_to(p, 16) && ld % 16 == 0 && stride % 16 == 0 && ld <= emu::kMaxTileLd;
+    }
+};
+const char *refused(const emu::BlockMMParams &p, int a_dtype, int w_dtype, int s_type, emu_dtype bias_dtype)
+{
+    if (p.M < 0 || p.N < 0 || p.K < 0 || p.E < 0) return "negative size";
+    if (!is_code(a_dtype) || !is_code(w_dtype)) return "a and w must be e4m3fn or e5m2";
+    if (!is_scale(s_type)) return "scales must be fp32 or e8m0";
+    if (!is_float(p.out_dtype)) return "out must be bf16, fp16 or fp32";
+    if (p.bias && bias_dtype != p.out_dtype && bias_dtype != EMU_DT_FP32) return "the bias must be of out's type or fp32";
+    return nullptr;
+}
+const char *refused_pointers(const emu::BlockMMParams &p, int s_type, emu_dtype bias_dtype)
+{
+    const int64_t blocks = blocks_of(p.K), wide = blocks_of(p.N);
+    if (!p.out || (p.K > 0 && p.E > 0 && (!p.a || !p.w || !p.sa || !p.sw))) return "null pointer";
+    if (bad_ld(p.ldo, p.N, p.M)) return "leading dimension smaller than a row";
+    if (p.K > 0 && p.E > 0) {
+        if (bad_ld(p.lda, p.K, p.M) || bad_ld(p.ldw, p.K, p.N)) return "leading dimension smaller than a row";
+        if (p.w_stride < 0 || p.sw_stride < 0 || far(p.w_stride, p.E) || far(p.sw_stride, p.E) || p.sa_row < 0 || p.sa_block < 0 ||
+            p.sw_row < 0 || p.sw_block < 0 || far(p.sa_row, p.M) || far(p.sa_block, blocks) || far(p.sw_row, wide) ||
+            far(p.sw_block, blocks))
+            return "a negative stride, or one too large";
+        if (!aligned_to(p.sa, scale_size(s_type)) || !aligned_to(p.sw, scale_size(s_type)))
+            return "a pointer is not aligned to its element";
+    }
+    if (!aligned_to(p.out, size_of(p.out_dtype)) || (p.bias && !aligned_to(p.bias, size_of(bias_dtype))))
+        return "a pointer is not aligned to its element";
+    return nullptr;
+}
+const char *too_large(const emu::BlockMMParams &p)
+{
+    if (p.M > kMaxRows || p.N > kMaxRows) return "more than 2^31-1 rows";
+    if (p.K > emu::kMaxTileLd) return "K above 2^22";
+    if ((p.M > 1 && p.sa_row > emu::kMaxScaleLd) || (p.N > EMU_BLOCK && p.sw_row > emu::kMaxScaleLd))
+        return "scales' rows more than 2^20 apart";
+    return nullptr;
+}
+emu_status block_mm(const emu::BlockMMParams &p, int a_dtype, int w_dtype, const void *ws, size_t bytes, hipStream_t stream)
+{
+    const bool a = Operand{p.a, p.lda, 0}.aligned(), w = Operand{p.w, p.ldw, p.w_stride}.aligned();
+    const int64_t need = emu::block_mm_workspace(p.M, p.N, p.K, p.E, p.ends != nullptr, p.out_dtype == EMU_DT_FP32, a, w);
+    if ((int64_t)bytes < need || (need > 0 && !ws)) return set_error(EMU_ERR_WORKSPACE, "workspace smaller than is needed");
+    if (!aligned_to(ws, 16)) return invalid("the workspace is not 16-byte aligned");
+    return done(emu::launch_block_mm(a_dtype, w_dtype, p, a, w, stream));
+}
 
 }  // namespace
 
@@ -117,6 +171,100 @@ emu_status emu_swiglu_block_backward(const void *g, emu_dtype g_dtype, int64_t l
     p.grad = grad;
     p.ldgrad = ldgrad;
     return done(emu::launch_swiglu_grad(g_dtype, q_dtype, s_type == EMU_SCALE_E8M0, p, stream));
+}
+
+size_t emu_block_scaled_mm_workspace(int64_t M, int64_t N, int64_t K, emu_dtype out_dtype, int a_aligned, int w_aligned)
+{
+    if (M <= 0 || N <= 0 || K <= 0 || M > kMaxRows || N > kMaxRows || K > emu::kMaxTileLd || !is_float(out_dtype)) return 0;
+    return (size_t)emu::block_mm_workspace(M, N, K, 1, false, out_dtype == EMU_DT_FP32, a_aligned != 0, w_aligned != 0);
+}
+
+emu_status emu_block_scaled_mm(const void *a, emu_dtype a_dtype, int64_t lda, const void *w, emu_dtype w_dtype, int64_t ldw,
+                               int64_t M, int64_t N, int64_t K, const void *scale_a, int64_t sa_row, int64_t sa_block,
+                               const void *scale_w, int64_t sw_row, int64_t sw_block, emu_scale_type s_type, const void *bias,
+                               emu_dtype bias_dtype, void *out, emu_dtype out_dtype, int64_t ldo, void *workspace,
+                               size_t workspace_bytes, hipStream_t stream)
+{
+    emu::BlockMMParams p{};
+    p.a = static_cast<const int8_t *>(a);
+    p.w = static_cast<const int8_t *>(w);
+    p.lda = lda;
+    p.ldw = ldw;
+    p.M = M;
+    p.N = N;
+    p.K = K;
+    p.sa = scale_a;
+    p.sw = scale_w;
+    p.sa_row = sa_row;
+    p.sa_block = sa_block;
+    p.sw_row = sw_row;
+    p.sw_block = sw_block;
+    p.e8m0 = s_type == EMU_SCALE_E8M0;
+    p.bias = bias;
+    p.bias_f32 = bias_dtype == EMU_DT_FP32;
+    p.out = out;
+    p.out_dtype = out_dtype;
+    p.ldo = ldo;
+    p.E = 1;
+    p.ws = workspace;
+    if (const char *text = refused(p, a_dtype, w_dtype, s_type, bias_dtype)) return invalid(text);
+    if (const char *text = too_large(p)) return unsupported(text);
+    if (M == 0 || N == 0) return set_error(EMU_OK, "");
+    if (const char *text = refused_pointers(p, s_type, bias_dtype)) return invalid(text);
+    return block_mm(p, a_dtype, w_dtype, workspace, workspace_bytes, stream);
+}
+
+size_t emu_grouped_block_scaled_mm_workspace(int64_t T, int64_t E, int64_t N, int64_t K, emu_dtype out_dtype, int a_aligned,
+                                             int w_aligned)
+{
+    if (T <= 0 || E <= 0 || N <= 0 || K <= 0 || T > kMaxGroupedRows || E > kMaxGroups || N > kMaxRows || K > emu::kMaxTileLd ||
+        !is_float(out_dtype))
+        return 0;
+    return (size_t)emu::block_mm_workspace(T, N, K, (int)E, true, out_dtype == EMU_DT_FP32, a_aligned != 0, w_aligned != 0);
+}
+
+emu_status emu_grouped_block_scaled_mm(const void *a, emu_dtype a_dtype, int64_t lda, const void *w, emu_dtype w_dtype,
+                                       int64_t ldw, int64_t w_stride, int64_t T, int64_t E, int64_t N, int64_t K,
+                                       const void *scale_a, int64_t sa_row, int64_t sa_block, const void *scale_w,
+                                       int64_t sw_row, int64_t sw_block, int64_t sw_stride, emu_scale_type s_type,
+                                       const void *ends, int ends_bits, int zero_rest, void *out, emu_dtype out_dtype,
+                                       int64_t ldo, void *workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    emu::BlockMMParams p{};
+    p.a = static_cast<const int8_t *>(a);
+    p.w = static_cast<const int8_t *>(w);
+    p.lda = lda;
+    p.ldw = ldw;
+    p.w_stride = E > 1 ? w_stride : 0;
+    p.M = T;
+    p.N = N;
+    p.K = K;
+    p.sa = scale_a;
+    p.sw = scale_w;
+    p.sa_row = sa_row;
+    p.sa_block = sa_block;
+    p.sw_row = sw_row;
+    p.sw_block = sw_block;
+    p.sw_stride = E > 1 ? sw_stride : 0;
+    p.e8m0 = s_type == EMU_SCALE_E8M0;
+    p.out = out;
+    p.out_dtype = out_dtype;
+    p.ldo = ldo;
+    p.ends = ends;
+    p.ends64 = ends_bits == 64;
+    p.E = E < 0 ? -1 : E > kMaxGroups ? (int)kMaxGroups : (int)E;
+    p.zero_rest = zero_rest != 0;
+    p.ws = workspace;
+    if (const char *text = refused(p, a_dtype, w_dtype, s_type, EMU_DT_FP32)) return invalid(text);
+    if (ends_bits != 32 && ends_bits != 64) return invalid("ends must be int32 or int64");
+    if (T > kMaxGroupedRows || E > kMaxGroups) return unsupported("T above 2^24 or E above 65536");
+    if (const char *text = too_large(p)) return unsupported(text);
+    if (T == 0 || N == 0 || (E == 0 && !zero_rest)) return set_error(EMU_OK, "");
+    if (!ends && E > 0) return invalid("null pointer");
+    if (!aligned_to(ends, ends_bits / 8)) return invalid("a pointer is not aligned to its element");
+    if (const char *text = refused_pointers(p, s_type, EMU_DT_FP32)) return invalid(text);
+    if (!ends) p.ends = out;  // (no group: never read, but the call is one by groups)
+    return block_mm(p, a_dtype, w_dtype, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"
