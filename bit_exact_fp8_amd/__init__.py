@@ -10,7 +10,7 @@ fails loudly if it is missing.
 """
 from .api import (EmuError, accumulate, abi_version, library_path, scaled_mm,  # noqa: F401
                   workspace_bytes)
-from .block_operators import (SwigluCodes, block_quant, block_scaled_mm, grouped_block_scaled_mm,  # noqa: F401
-                              swiglu_block_backward, swiglu_block_quant)
+from .block_operators import (SwigluCodes, block_quant, block_scaled_mm, block_weight_grad,  # noqa: F401
+                              grouped_block_scaled_mm, swiglu_block_backward, swiglu_block_quant)
 from .operators import (TokenLogprobs, add_rms_norm_backward, add_rms_norm_quant, int8_scaled_mm,  # noqa: F401
                         token_logprobs, token_logprobs_backward)

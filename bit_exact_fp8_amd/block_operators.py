@@ -5,7 +5,8 @@
 ``swiglu_block_quant`` / ``swiglu_block_backward``: the gated activation with
 its codes, and its gradient from the codes that gate and up were kept in.
 ``block_scaled_mm`` / ``grouped_block_scaled_mm``: the product of such codes,
-also by groups of rows with weights of their own.
+also by groups of rows with weights of their own.  ``block_weight_grad``: the
+gradient of a product's weights from the codes that its input was kept in.
 
 A value's code times its block's scale stands for the value.  Codes are
 float8_e4m3fn or float8_e5m2; scales float32, or float8_e8m0fnu, powers of two,
@@ -45,6 +46,10 @@ def _lib():
                                                     i64, i64, i32, vp, i32, i32, vp, i32, i64, vp, sz, vp]
         lib.emu_grouped_block_scaled_mm_workspace.argtypes = [i64, i64, i64, i64, i32, i32, i32]
         lib.emu_grouped_block_scaled_mm_workspace.restype = sz
+        lib.emu_block_weight_grad.argtypes = [vp, i32, i64, vp, i32, i64, vp, i64, i64, i64, i64, i64, vp, i32, i64, vp, i32, i64,
+                                              i64, vp, sz, vp]
+        lib.emu_block_weight_grad_workspace.argtypes = [i64, i64, i64, i64, i32, i32, i32]
+        lib.emu_block_weight_grad_workspace.restype = sz
         _LIB = lib
     return _LIB
 
@@ -129,3 +134,17 @@ def grouped_block_scaled_mm(mat1: torch.Tensor, mat2: torch.Tensor, scale_a: tor
     one past the rows as the last row's.  Groups may be empty.  Rows behind the
     last group's are 0, and in an ``out`` that is given left as they are."""
     return (_OPS or _binding()).grouped_block_scaled_mm(mat1, mat2, scale_a, scale_b, ends, out_dtype, out)
+
+
+def block_weight_grad(grad: torch.Tensor, codes: torch.Tensor, scale: torch.Tensor, ends: torch.Tensor | None = None,
+                      out_dtype=None, out: torch.Tensor | None = None) -> torch.Tensor:
+    """``grad.T @ x`` over the rows, [N, K], with x what the codes of a product's input stand for.
+
+    grad [..., N] of any of the three types; codes [..., K] and scale [...,
+    blocks of K] as ``block_quant`` gives them, scales float8_e8m0fnu (powers of
+    two, under which bf16 holds x exactly).  ends [E]: a sum for each group of
+    rows, [E, N, K], as in ``grouped_block_scaled_mm``; rows behind the last
+    group's take no part, and an empty group's sum is 0.  Products are exact and
+    added in float32; out_dtype is grad's where none is given.  grad in float16
+    or float32 takes two or three times as long as in bfloat16."""
+    return (_OPS or _binding()).block_weight_grad(grad, codes, scale, ends, out_dtype, out)

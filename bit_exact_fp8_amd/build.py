@@ -7,7 +7,7 @@ dispatcher, the combine kernel, the deferred-infinity kernels
 (emu_specials.hip), the no-allocation entry point (emu_noalloc.hip), the C
 ABI and the operators beside the product (emu_norm.hip, emu_int8.hip,
 emu_logprobs.hip, ops_api.cpp), those on codes with a scale for each block of
-128 among them (emu_block_*.hip, ops_block_api.cpp).  The operators' Python calls (ops_binding.cpp)
+128 among them (emu_block_*.hip, emu_weight_grad.hip, ops_block_api.cpp).  The operators' Python calls (ops_binding.cpp)
 are a module of their own, _ops.so."""
 from __future__ import annotations
 
@@ -46,7 +46,7 @@ def _units(objdir: str):
              (os.path.join(CSRC, "emu_noalloc.hip"), os.path.join(objdir, "emu_noalloc.o"), []),
              (os.path.join(CSRC, "emu_api.cpp"), os.path.join(objdir, "emu_api.o"), [])]
     for name in ("emu_norm.hip", "emu_int8.hip", "emu_logprobs.hip", "ops_api.cpp", "emu_block_quant.hip",
-                 "emu_block_plan.hip", "ops_block_api.cpp"):
+                 "emu_block_plan.hip", "emu_weight_grad.hip", "ops_block_api.cpp"):
         extra = MFMA_FLAGS if name == "emu_int8.hip" else []
         units.append((os.path.join(CSRC, name), os.path.join(objdir, name.split(".")[0] + ".o"), extra))
     for af, wf in ((0, 0), (0, 1), (1, 0), (1, 1)):

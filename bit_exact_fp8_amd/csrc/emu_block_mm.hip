@@ -115,26 +115,6 @@ __device__ __forceinline__ void write_zeros(const BlockMMParams &p, const TileRo
 
 // ---- products and outputs ------------------------------------------------
 
-// What is the same for all lanes, known to be so.
-__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-__device__ __forceinline__ int64_t uniform(int64_t v)
-{
-    return (int64_t)(((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32) | (uint32_t)uniform((int)v));
-}
-
-template <int F>
-__device__ __forceinline__ uint32_t two_bf16(uint32_t codes, bool high)
-{
-    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-    bf16x2 v;
-    if (F == 0)
-        v = high ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, 1.0f, true)
-                 : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, 1.0f, false);
-    else
-        v = high ? __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(codes, 1.0f, true)
-                 : __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(codes, 1.0f, false);
-    return __builtin_bit_cast(uint32_t, v);
-}
 // 32 codes of a lane in bf16, which holds each exactly.
 struct Wide {
     bf16x8 v[4];
@@ -148,8 +128,8 @@ __device__ __forceinline__ Wide in_bf16(const i32x8 &codes)
         i32x4 r;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            r[2 * h] = (int)two_bf16<F>((uint32_t)codes[2 * q + h], false);
-            r[2 * h + 1] = (int)two_bf16<F>((uint32_t)codes[2 * q + h], true);
+            r[2 * h] = (int)two_bf16<F>((uint32_t)codes[2 * q + h], false, 1.0f);
+            r[2 * h + 1] = (int)two_bf16<F>((uint32_t)codes[2 * q + h], true, 1.0f);
         }
         w.v[q] = __builtin_bit_cast(bf16x8, r);
     }
@@ -460,41 +440,8 @@ __global__ __launch_bounds__(WM * WN * 64, (TileShape<MODE, BM, BN, WM, WN, NB>:
     f32x4 bias[FN];
 #pragma unroll
     for (int j = 0; j < FN; ++j) bias[j] = bias_at(p, n + j * 16);
-    // Outputs of 16 bits go out eight to a lane: the quarters of a wave swap
-    // halves between two fragments, and a store then writes 64 bytes of each of
-    // 16 rows, not 32.
     const bool whole = rows == BM && cols == BN;
-    with_type(p.out_dtype, [&](auto *type) {
-        typedef std::remove_pointer_t<decltype(type)> E;
-        const int quarter = lane >> 4;
-        const int64_t n8 = n0 + wn + (quarter & 1) * 16 + (quarter >> 1) * 8;
-        E *out = static_cast<E *>(p.out) + m * p.ldo;
-#pragma unroll
-        for (int i = 0; i < FM; ++i, out += 16 * p.ldo) {
-            const bool in = whole || m + i * 16 < at.end;
-#pragma unroll
-            for (int j = 0; j < FN; j += 2) {
-                f32x4 x = acc[i][j], y = acc[i][j + 1];
-                if (p.bias) x += bias[j], y += bias[j + 1];
-                const Four<E> v = __builtin_convertvector(x, Four<E>), w = __builtin_convertvector(y, Four<E>);
-                if constexpr (sizeof(E) == 2) {
-                    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-                    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-                    typedef E e8 __attribute__((ext_vector_type(8)));
-                    const u32x2 a = __builtin_bit_cast(u32x2, v), b = __builtin_bit_cast(u32x2, w);
-                    const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
-                    const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
-                    const u32x4 out8 = {c[0], d[0], c[1], d[1]};
-                    const int64_t to = n8 + j * 16;
-                    if (in) store_valid(out + to, __builtin_bit_cast(e8, out8), whole ? 8 : p.N - to);
-                } else if (in) {
-                    const int64_t to = n + j * 16;
-                    store_valid(out + to, v, whole ? 4 : p.N - to);
-                    store_valid(out + to + 16, w, whole ? 4 : p.N - to - 16);
-                }
-            }
-        }
-    });
+    store_tile(p.out, p.out_dtype, p.ldo, acc, p.bias ? bias : nullptr, m, at.end, n0 + wn, p.N, lane, whole);
 }
 
 // ---- few rows --------------------------------------------------------------

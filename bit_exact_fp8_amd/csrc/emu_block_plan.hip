@@ -143,22 +143,6 @@ bool in_words(const BlockMMParams &p)
     return ((reinterpret_cast<uintptr_t>(p.a) | reinterpret_cast<uintptr_t>(p.w) | p.lda | p.ldw | p.w_stride) & 3) == 0;
 }
 
-// `out`: 16-byte aligned
-void repack(const int8_t *in, int64_t ld, int64_t stride, int64_t per, int64_t total, int64_t K, int8_t *out, int64_t ldo,
-            hipStream_t stream)
-{
-    const int rows = (int)ceil_div(512, ldo / 16);  // some two chunks a thread
-    constexpr int64_t most = int64_t(1) << 22;      // workgroups of a launch
-    for (int64_t r = 0; r < total; r += most * rows) {
-        const int64_t left = ceil_div(total - r, rows);
-        const dim3 grid((unsigned)(left < most ? left : most));
-        if (((reinterpret_cast<uintptr_t>(in) | ld | stride) & 3) == 0)
-            hipLaunchKernelGGL((block_repack<true>), grid, dim3(256), 0, stream, in, ld, stride, per, total, K, out, ldo, r, rows);
-        else
-            hipLaunchKernelGGL((block_repack<false>), grid, dim3(256), 0, stream, in, ld, stride, per, total, K, out, ldo, r, rows);
-    }
-}
-
 void launch_slice(int a_dtype, int w_dtype, BlockMMParams p, bool a_aligned, bool w_aligned, hipStream_t stream)
 {
     const dim3 quads((unsigned)ceil_div(p.M * ceil_div(p.N, 4), 256));
@@ -171,13 +155,13 @@ void launch_slice(int a_dtype, int w_dtype, BlockMMParams p, bool a_aligned, boo
     k.words = in_words(p);
     char *ws = static_cast<char *>(p.ws);
     if (plan.repack_a) {
-        repack(p.a, p.lda, 0, p.M, p.M, p.K, reinterpret_cast<int8_t *>(ws), plan.ld, stream);
+        repack_codes(p.a, p.lda, 0, p.M, p.M, p.K, reinterpret_cast<int8_t *>(ws), plan.ld, stream);
         p.a = reinterpret_cast<const int8_t *>(ws);
         p.lda = plan.ld;
     }
     if (plan.repack_w) {
         int8_t *w = reinterpret_cast<int8_t *>(ws + plan.a_bytes);
-        repack(p.w, p.ldw, p.w_stride, p.N, p.E * p.N, p.K, w, plan.ld, stream);
+        repack_codes(p.w, p.ldw, p.w_stride, p.N, p.E * p.N, p.K, w, plan.ld, stream);
         p.w = w;
         p.ldw = plan.ld;
         p.w_stride = p.N * plan.ld;
@@ -192,6 +176,21 @@ void launch_slice(int a_dtype, int w_dtype, BlockMMParams p, bool a_aligned, boo
 }
 
 }  // namespace
+
+void repack_codes(const int8_t *in, int64_t ld, int64_t stride, int64_t per, int64_t total, int64_t K, int8_t *out, int64_t ldo,
+                  hipStream_t stream)
+{
+    const int rows = (int)ceil_div(512, ldo / 16);  // some two chunks a thread
+    constexpr int64_t most = int64_t(1) << 22;      // workgroups of a launch
+    for (int64_t r = 0; r < total; r += most * rows) {
+        const int64_t left = ceil_div(total - r, rows);
+        const dim3 grid((unsigned)(left < most ? left : most));
+        if (((reinterpret_cast<uintptr_t>(in) | ld | stride) & 3) == 0)
+            hipLaunchKernelGGL((block_repack<true>), grid, dim3(256), 0, stream, in, ld, stride, per, total, K, out, ldo, r, rows);
+        else
+            hipLaunchKernelGGL((block_repack<false>), grid, dim3(256), 0, stream, in, ld, stride, per, total, K, out, ldo, r, rows);
+    }
+}
 
 int64_t block_mm_workspace(int64_t M, int64_t N, int64_t K, int E, bool grouped, bool fp32_out, bool a_aligned, bool w_aligned)
 {

@@ -747,6 +747,72 @@ PyObject *grouped_block_scaled_mm(PyObject *const *a)
     return given ? held(a[6]) : wrap(o.own);
 }
 
+// grad, codes, scale, ends, out_dtype, out
+PyObject *block_weight_grad(PyObject *const *a)
+{
+    outside_autograd({a[0], a[1], a[2]}, {a[5]});
+    const Tensor &g = gpu("grad", a[0]), &x = tensor("codes", a[1]), &s = tensor("scale", a[2]);
+    const Tensor *ends = optional("ends", a[3]), *given = optional("out", a[5]);
+    floating("grad", g);
+    codes("codes", x);
+    if (s.scalar_type() != ScalarType::Float8_e8m0fnu)
+        type_error("scale must be float8_e8m0fnu (powers of two), not " + str(s.scalar_type()));
+    if (g.dim() < 2 || x.dim() < 2) value_error("grad and codes must be matrices of rows");
+    const Rows r = rows("grad", g), c = rows("codes", x);
+    on_device("codes", x, g.device());
+    if (g.sizes().slice(0, g.dim() - 1) != x.sizes().slice(0, x.dim() - 1))
+        value_error("codes must have grad's rows " + str(g.sizes().slice(0, g.dim() - 1)) + ", not " +
+                    str(x.sizes().slice(0, x.dim() - 1)));
+    c10::SmallVector<int64_t, 6> shape(x.sizes().begin(), x.sizes().end());
+    shape.back() = blocks_of(c.n);
+    shaped("scale", s, shape, g.device());
+    int64_t s_row = 0, s_block = c.n > EMU_BLOCK ? s.stride(s.dim() - 1) : 0;
+    if (s.dim() == 2) {
+        if (c.T > 1) s_row = s.stride(0);
+    } else {
+        if (!s.is_contiguous()) value_error("scale of more than two axes must be dense");
+        s_row = blocks_of(c.n);
+    }
+    int64_t E = 0;
+    int bits = 32;
+    if (ends) {
+        if (ends->dim() != 1) value_error("ends must be a dense vector");
+        E = ends->size(0);
+        bits = ends_bits(*ends, E, g.device());
+    }
+    const ScalarType dtype = a[4] == Py_None ? g.scalar_type() : dtype_of(a[4], is_float);
+    c10::SmallVector<int64_t, 3> out_shape;
+    if (ends) out_shape.push_back(E);
+    out_shape.push_back(r.n);
+    out_shape.push_back(c.n);
+    Tensor own;
+    int64_t ldo = c.n, stride = r.n * c.n;
+    if (given) {
+        shaped("out", *given, out_shape, g.device());
+        if (given->scalar_type() != dtype) type_error("out must be of out_dtype");
+        const int64_t d = given->dim();
+        if (given->numel() && c.n > 1 && given->stride(d - 1) != 1) value_error("out must be row-major");
+        if (given->numel() && r.n > 1) ldo = given->stride(d - 2);
+        if (given->numel() && E > 1) stride = given->stride(0);
+    } else {
+        own = empty(out_shape, g, dtype);
+    }
+    const int64_t unit = 16 / g.element_size();
+    const auto at = [](const Tensor &t) { return reinterpret_cast<uintptr_t>(t.data_ptr()); };
+    const bool ga = !(at(g) & 15) && r.ld % unit == 0 && r.ld <= EMU_BLOCK_MAX_ALIGNED_LD,
+               ca = !(at(x) & 15) && c.ld % 16 == 0 && c.ld <= EMU_BLOCK_MAX_ALIGNED_LD;
+    if (ends && E == 0) return given ? held(a[5]) : wrap(own);
+    const size_t bytes = emu_block_weight_grad_workspace(r.T, E, r.n, c.n, code(g), ga, ca);
+    const Tensor ws = workspace(bytes, g);
+    launch(g.device(), [&](hipStream_t stream) {
+        return emu_block_weight_grad(ptr(g), code(g), r.ld, ptr(x), code(x), c.ld, ptr(s), s_row, s_block, r.T, r.n, c.n,
+                                     ptr(ends), bits, E, given ? ptr(given) : ptr(own),
+                                     static_cast<emu_dtype>(code_of(dtype)), ldo, stride, ptr(ws), bytes, stream);
+    });
+    if (given) written(*given);
+    return given ? held(a[5]) : wrap(own);
+}
+
 template <PyObject *(*call)(PyObject *const *), int N>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t nargs)
 {
@@ -784,6 +850,7 @@ PyMethodDef g_methods[] = {
     {"swiglu_block_backward", function<swiglu_block_backward, 3>(), METH_FASTCALL, nullptr},
     {"block_scaled_mm", function<block_scaled_mm, 7>(), METH_FASTCALL, nullptr},
     {"grouped_block_scaled_mm", function<grouped_block_scaled_mm, 7>(), METH_FASTCALL, nullptr},
+    {"block_weight_grad", function<block_weight_grad, 6>(), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_ops", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

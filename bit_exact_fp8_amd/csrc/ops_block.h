@@ -69,6 +69,34 @@ constexpr int64_t kMaxTileLd = EMU_BLOCK_MAX_ALIGNED_LD, kMaxScaleLd = int64_t(1
 int64_t block_mm_workspace(int64_t M, int64_t N, int64_t K, int E, bool grouped, bool fp32_out, bool a_aligned, bool w_aligned);
 hipError_t launch_block_mm(int a_dtype, int w_dtype, const BlockMMParams &p, bool a_aligned, bool w_aligned, hipStream_t stream);
 
+// The weights' gradient, of all rows (E = 0) or of each of E groups.  g is
+// bf16 in `planes` planes, whose sum it stands for.
+struct WeightGradParams {
+    const uint16_t *g;
+    int64_t ldg, plane_stride;
+    int planes;
+    const int8_t *codes;
+    int64_t ldc;
+    const uint8_t *scales;
+    int64_t s_row, s_block;
+    int64_t T, N, K;
+    const void *ends;
+    int ends64;
+    int E;
+    void *out;
+    int out_dtype;
+    int64_t ldo, out_stride;
+};
+int64_t weight_grad_workspace(int64_t T, int E, int64_t N, int64_t K, int g_dtype, bool g_aligned, bool c_aligned);
+// p.g: of g_dtype
+hipError_t launch_weight_grad(int g_dtype, int c_dtype, const WeightGradParams &p, bool g_aligned, bool c_aligned, void *ws,
+                              hipStream_t stream);
+
+// Rows of `count` matrices laid out anew, 16-byte aligned, with the leading
+// dimension `ldo`, a multiple of 128, and zeros past K.
+void repack_codes(const int8_t *in, int64_t ld, int64_t stride, int64_t per, int64_t total, int64_t K, int8_t *out, int64_t ldo,
+                  hipStream_t stream);
+
 // The kernels of one pair of codes' types (emu_block_mm.hip).
 enum BlockMode {
     kHardware,  // e8m0 scales go into the matrix instruction
@@ -92,6 +120,21 @@ void launch_block_kernel(const BlockMMParams &p, const BlockPlan &plan, float *p
 __device__ __forceinline__ float e8m0_value(uint32_t b)
 {
     return __uint_as_float(b == 0 ? 0x00400000u : b == 255 ? 0x7FC00000u : b << 23);
+}
+
+// Two of four codes (F: 0 e4m3fn, 1 e5m2) times a power of two, in bf16.
+template <int F>
+__device__ __forceinline__ uint32_t two_bf16(uint32_t codes, bool high, float scale)
+{
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    bf16x2 v;
+    if (F == 0)
+        v = high ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, scale, true)
+                 : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, scale, false);
+    else
+        v = high ? __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(codes, scale, true)
+                 : __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(codes, scale, false);
+    return __builtin_bit_cast(uint32_t, v);
 }
 
 #endif

@@ -76,6 +76,13 @@ const char *too_large(const emu::BlockMMParams &p)
         return "scales' rows more than 2^20 apart";
     return nullptr;
 }
+const char *grad_too_large(int64_t T, int64_t E, int64_t N, int64_t K)
+{
+    if (T > int64_t(1) << 30 || E > kMaxGroups) return "T above 2^30 or E above 65536";
+    if (N > emu::kMaxTileLd || K > emu::kMaxTileLd) return "N or K above 2^22";
+    if (blocks_of(N) * blocks_of(K) > (int64_t(1) << 23) / (E ? E : 1)) return "more than 2^23 tiles of 128 x 128";
+    return nullptr;
+}
 emu_status block_mm(const emu::BlockMMParams &p, int a_dtype, int w_dtype, const void *ws, size_t bytes, hipStream_t stream)
 {
     const bool a = Operand{p.a, p.lda, 0}.aligned(), w = Operand{p.w, p.ldw, p.w_stride}.aligned();
@@ -265,6 +272,62 @@ emu_status emu_grouped_block_scaled_mm(const void *a, emu_dtype a_dtype, int64_t
     if (const char *text = refused_pointers(p, s_type, EMU_DT_FP32)) return invalid(text);
     if (!ends) p.ends = out;  // (no group: never read, but the call is one by groups)
     return block_mm(p, a_dtype, w_dtype, workspace, workspace_bytes, stream);
+}
+
+size_t emu_block_weight_grad_workspace(int64_t T, int64_t E, int64_t N, int64_t K, emu_dtype g_dtype, int g_aligned,
+                                       int c_aligned)
+{
+    if (T < 0 || E < 0 || N <= 0 || K <= 0 || !is_float(g_dtype) || grad_too_large(T, E, N, K)) return 0;
+    return (size_t)emu::weight_grad_workspace(T, (int)E, N, K, g_dtype, g_aligned != 0, c_aligned != 0);
+}
+
+emu_status emu_block_weight_grad(const void *g, emu_dtype g_dtype, int64_t ldg, const void *codes, emu_dtype c_dtype,
+                                 int64_t ldc, const void *scales, int64_t s_row, int64_t s_block, int64_t T, int64_t N,
+                                 int64_t K, const void *ends, int ends_bits, int64_t E, void *out, emu_dtype out_dtype,
+                                 int64_t ldo, int64_t out_stride, void *workspace, size_t workspace_bytes,
+                                 hipStream_t stream)
+{
+    if (T < 0 || N < 0 || K < 0 || E < 0) return invalid("negative size");
+    if (!is_float(g_dtype)) return invalid("g must be bf16, fp16 or fp32");
+    if (!is_code(c_dtype)) return invalid("codes must be e4m3fn or e5m2");
+    if (!is_float(out_dtype)) return invalid("out must be bf16, fp16 or fp32");
+    if (ends ? ends_bits != 32 && ends_bits != 64 : E != 0) return invalid("ends must be int32 or int64, and null without groups");
+    if (ends && E == 0) return set_error(EMU_OK, "");
+    if (const char *text = grad_too_large(T, E, N, K)) return unsupported(text);
+    if (N == 0 || K == 0) return set_error(EMU_OK, "");
+    if (!out || (T > 0 && (!g || !codes || !scales))) return invalid("null pointer");
+    if (bad_ld(ldo, K, N) || out_stride < 0 || (E > 1 && (out_stride < 1 || far(out_stride, E))))
+        return invalid("leading dimension smaller than a row, or a bad stride");
+    if (T > 0 && (bad_ld(ldg, N, T) || bad_ld(ldc, K, T))) return invalid("leading dimension smaller than a row");
+    if (T > 0 && (s_row < 0 || s_block < 0 || far(s_row, T) || far(s_block, blocks_of(K)))) return invalid("a negative stride, or one too large");
+    const size_t size = size_of(g_dtype);
+    if (!aligned_to(g, size) || !aligned_to(out, size_of(out_dtype)) || (ends && !aligned_to(ends, ends_bits / 8)))
+        return invalid("a pointer is not aligned to its element");
+    const bool ga = aligned_to(g, 16) && ldg % (int64_t)(16 / size) == 0 && ldg <= emu::kMaxTileLd;
+    const bool ca = aligned_to(codes, 16) && ldc % 16 == 0 && ldc <= emu::kMaxTileLd;
+    const int64_t need = emu::weight_grad_workspace(T, (int)E, N, K, g_dtype, ga, ca);
+    if ((int64_t)workspace_bytes < need || (need > 0 && !workspace))
+        return set_error(EMU_ERR_WORKSPACE, "workspace smaller than emu_block_weight_grad_workspace");
+    if (!aligned_to(workspace, 16)) return invalid("the workspace is not 16-byte aligned");
+    emu::WeightGradParams p{};
+    p.g = static_cast<const uint16_t *>(g);
+    p.ldg = ldg;
+    p.codes = static_cast<const int8_t *>(codes);
+    p.ldc = ldc;
+    p.scales = static_cast<const uint8_t *>(scales);
+    p.s_row = s_row;
+    p.s_block = s_block;
+    p.T = T;
+    p.N = N;
+    p.K = K;
+    p.ends = ends;
+    p.ends64 = ends_bits == 64;
+    p.E = (int)E;
+    p.out = out;
+    p.out_dtype = out_dtype;
+    p.ldo = ldo;
+    p.out_stride = out_stride;
+    return done(emu::launch_weight_grad(g_dtype, c_dtype, p, ga, ca, workspace, stream));
 }
 
 }  // extern "C"

@@ -46,6 +46,13 @@ __device__ __forceinline__ void with_type(int dtype, F f)
 
 constexpr int kStage = 128;  // codes of K at a time
 
+// What is the same for all lanes, known to be so.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform(int64_t v)
+{
+    return (int64_t)(((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32) | (uint32_t)uniform((int)v));
+}
+
 // LDS holds a stage's rows of 128 bytes as eight chunks of 16; row r's chunk c
 // stands at place c ^ swizzle(r), which spreads the 16 rows that a
 // ds_read_b128 meets over all banks.
@@ -129,6 +136,48 @@ __device__ __forceinline__ i32x4 load16(const int8_t *row, int64_t k, int64_t K)
     if (over <= 0) return v;
     const unsigned __int128 bits = __builtin_bit_cast(unsigned __int128, v);
     return over < 16 ? __builtin_bit_cast(i32x4, bits >> (8 * (int)over)) : i32x4{0, 0, 0, 0};
+}
+
+// A wave's outputs: fragment (i, j) holds the outputs of row m + 16 i from
+// column n + 16 j + 4 (lane / 16) on, four to a lane; `whole`: all of them lie
+// within the matrix.  Outputs of 16 bits go out eight to a lane: the quarters of
+// a wave swap halves between two fragments, and a store then writes 64 bytes
+// of each of 16 rows, not 32.
+template <int FM, int FN>
+__device__ __forceinline__ void store_tile(void *to, int dtype, int64_t ld, const f32x4 (&acc)[FM][FN], const f32x4 *bias, int64_t m,
+                                           int64_t rows, int64_t n, int64_t cols, int lane, bool whole)
+{
+    with_type(dtype, [&](auto *type) {
+        typedef std::remove_pointer_t<decltype(type)> E;
+        const int quarter = lane >> 4;
+        const int64_t n4 = n + quarter * 4, n8 = n + (quarter & 1) * 16 + (quarter >> 1) * 8;
+        E *out = static_cast<E *>(to) + m * ld;
+#pragma unroll
+        for (int i = 0; i < FM; ++i, out += 16 * ld) {
+            const bool in = whole || m + i * 16 < rows;
+#pragma unroll
+            for (int j = 0; j < FN; j += 2) {
+                f32x4 x = acc[i][j], y = acc[i][j + 1];
+                if (bias) x += bias[j], y += bias[j + 1];
+                const Four<E> v = __builtin_convertvector(x, Four<E>), w = __builtin_convertvector(y, Four<E>);
+                if constexpr (sizeof(E) == 2) {
+                    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+                    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+                    typedef E e8 __attribute__((ext_vector_type(8)));
+                    const u32x2 a = __builtin_bit_cast(u32x2, v), b = __builtin_bit_cast(u32x2, w);
+                    const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+                    const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+                    const u32x4 both = {c[0], d[0], c[1], d[1]};
+                    const int64_t at = n8 + j * 16;
+                    if (in) store_valid(out + at, __builtin_bit_cast(e8, both), whole ? 8 : cols - at);
+                } else if (in) {
+                    const int64_t at = n4 + j * 16;
+                    store_valid(out + at, v, whole ? 4 : cols - at);
+                    store_valid(out + at + 16, w, whole ? 4 : cols - at - 16);
+                }
+            }
+        }
+    });
 }
 
 }  // namespace emu

@@ -137,6 +137,36 @@ EMU_API emu_status emu_grouped_block_scaled_mm(const void *a, emu_dtype a_dtype,
 EMU_API size_t emu_grouped_block_scaled_mm_workspace(int64_t T, int64_t E, int64_t N, int64_t K, emu_dtype out_dtype,
                                                      int a_aligned, int w_aligned);
 
+/*
+ * The gradient of a product's weights from the codes that its input was kept
+ * in: out[n, k] = sum over rows t of g[t, n] x[t, k], x what codes and scales
+ * stand for, in bf16 (which holds it exactly, but for values below 2^-133 or
+ * beyond the type's largest).
+ *
+ * g [T, N] bf16, fp16 or fp32; codes [T, K] e4m3fn or e5m2, blocks of 1 x 128
+ * with e8m0 scales, that of row t and block b at t s_row + b s_block; out of
+ * any of g's types.  Products are exact (those of fp16 and fp32 g as two and
+ * three parts) and added in binary32; an out of no rows is 0.
+ * ends NULL: one sum over all rows, out [N, K].  Else E sums by groups of
+ * rows, as in emu_grouped_block_scaled_mm: out [E, N, K], out_stride elements
+ * between matrices, and rows behind the last group's take no part.
+ * workspace: emu_block_weight_grad_workspace(...) bytes, 16-byte aligned (E =
+ * 0: no groups); `aligned` says that the pointer and the rows' distance in
+ * bytes are multiples of 16 and the leading dimension is at most
+ * EMU_BLOCK_MAX_ALIGNED_LD.
+ * T up to 2^30, N and K to EMU_BLOCK_MAX_ALIGNED_LD, E to 65536, and at most
+ * 2^23 tiles of 128 x 128 in all.
+ */
+EMU_API emu_status emu_block_weight_grad(const void *g, emu_dtype g_dtype, int64_t ldg,
+                                         const void *codes, emu_dtype c_dtype, int64_t ldc,
+                                         const void *scales, int64_t s_row, int64_t s_block,
+                                         int64_t T, int64_t N, int64_t K,
+                                         const void *ends, int ends_bits, int64_t E,
+                                         void *out, emu_dtype out_dtype, int64_t ldo, int64_t out_stride,
+                                         void *workspace, size_t workspace_bytes, hipStream_t stream);
+EMU_API size_t emu_block_weight_grad_workspace(int64_t T, int64_t E, int64_t N, int64_t K, emu_dtype g_dtype,
+                                               int g_aligned, int c_aligned);
+
 #ifdef __cplusplus
 }
 #endif

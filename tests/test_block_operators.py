@@ -592,6 +592,129 @@ def test_grouped_empty(dev):
     assert fw.grouped_block_scaled_mm(z(5, 64), z(2, 0, 64).transpose(1, 2), e(5, 1), e(2, 1, 0), ends).shape == (5, 0)
 
 
+# ---- the weights' gradient --------------------------------------------------------
+def check_weight_grad(dev, T, N, K, g_t=BF, c_t=E4, out=None, ends=None, bits=torch.int32, pad=(0, 0), exact=False, given=False,
+                      turned=False, seed=0):
+    gen = rng(seed + T + 3 * N + 7 * K)
+    if exact:
+        c, s, v = exact_codes(gen, T, K, 1, c_t, E8)
+        g = torch.randint(-2, 3, (T, N), generator=gen).to(g_t)
+    else:
+        c, s, v = make_codes(gen, T, K, 1, c_t, E8)
+        g = rand(gen, T, N, std=0.1, dtype=g_t)
+    o_t = out or g_t
+    note(f"weights' gradient {T}x{N}x{K} {g_t} {c_t} {o_t} ends={ends and ends[:6]} pad={pad} exact={exact} given={given}")
+    shape = (N, K) if ends is None else (len(ends), N, K)
+    sd = s.to(dev)
+    if turned:
+        sd = sd.view(torch.uint8).t().contiguous().t().view(E8)
+    o = torch.full((*shape[:-1], K + 3), 7.0, dtype=o_t, device=dev)[..., 2:2 + K] if given else None
+    e = None if ends is None else torch.tensor(ends, dtype=bits, device=dev)
+    y = fw.block_weight_grad(wide(g, pad[0], dev), as_rows(c, pad[1], dev), sd, e, out_dtype=out, out=o)
+    torch.cuda.synchronize(dev)
+    assert y.shape == shape and y.dtype == o_t
+    gd, v = g.to(dev).to(f64), v.to(dev)
+    for i, (first, end) in enumerate(spans(ends, T) if ends is not None else [(0, T)]):
+        x, h = v[first:end], gd[first:end]
+        want = h.t().contiguous() @ x
+        got = y if ends is None else y[i]
+        if exact:
+            assert not want.numel() or float(want.abs().max()) < 2 ** 24
+            assert torch.equal(got, want.float().to(o_t)), (i, (got != want.float().to(o_t)).nonzero()[:4].tolist())
+        else:
+            close(got, want, half_step(want, o_t) + F * (h.abs().t().contiguous() @ x.abs()), "weights' gradient")
+    if given:
+        assert (o._base[..., :2] == 7).all() and (o._base[..., 2 + K:] == 7).all()
+
+
+GRAD = [(1, 1, 1), (1, 128, 128), (63, 130, 129), (64, 8, 200), (65, 300, 7), (129, 128, 256), (500, 257, 513), (1023, 1925, 1920),
+        (4000, 200, 300), (2000, 1100, 2100), (300, 4100, 4000), (0, 40, 50)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,N,K", GRAD)
+@pytest.mark.parametrize("g_t,c_t,out", [(BF, E4, None), (HF, E5, SF), (SF, E4, None), (BF, E5, SF), (SF, E5, BF), (HF, E4, HF)])
+def test_weight_grad(dev, T, N, K, g_t, c_t, out):
+    check_weight_grad(dev, T, N, K, g_t, c_t, out)
+    check_weight_grad(dev, T, N, K, g_t, c_t, out, exact=True, given=True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,E,N,K", [(5, 3, 40, 100), (100, 7, 130, 256), (1000, 130, 96, 384), (3000, 9, 500, 640), (6000, 4, 1030, 272),
+                                     (2500, 64, 250, 528), (9000, 2, 2048, 1536)])
+@pytest.mark.parametrize("g_t,out,bits", [(BF, None, torch.int32), (HF, SF, torch.int64), (SF, BF, torch.int32)])
+def test_weight_grad_by_groups(dev, T, E, N, K, g_t, out, bits):
+    ends = random_ends(rng(T + E), T, E)
+    check_weight_grad(dev, T, N, K, g_t, E4, out, ends, bits)
+    check_weight_grad(dev, T, N, K, g_t, E5, out, ends, bits, exact=True, given=True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,N,K", [(50, 40, 256), (900, 300, 400)])
+@pytest.mark.parametrize("ends", [[], [0, 0, 0], [0, 50, 50], [50], [10 ** 9], [-5, 20, 7, 30, -1], [1, 2, 3], [40, 2 ** 31 - 1, 0],
+                                  [0] * 63 + [9] + [9] * 64 + [31], [3] * 200])
+def test_weight_grad_ends(dev, T, N, K, ends):
+    check_weight_grad(dev, T, N, K, ends=ends, exact=True)
+    check_weight_grad(dev, T, N, K, SF, ends=[10 ** 12 if e == 10 ** 9 else e for e in ends], bits=torch.int64, exact=True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("pad", [(3, 0), (0, 5), (8, 16), (7, 15), (16, 3)])
+@pytest.mark.parametrize("T,N,K", [(40, 70, 208), (700, 130, 333), (1500, 300, 272)])
+def test_weight_grad_strides(dev, T, N, K, pad):
+    check_weight_grad(dev, T, N, K, pad=pad, exact=True, turned=True)
+    check_weight_grad(dev, T, N, K, BF, E5, SF, random_ends(rng(T), T, 5), pad=pad, turned=True, given=True)
+    check_weight_grad(dev, T, N, K, HF, pad=pad)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("g_t", [BF, HF, SF])
+def test_weight_grad_special_values(dev, g_t):
+    """Infinities and NaN stay in their groups, columns and blocks; rows behind the last group take no part."""
+    gen = rng(2)
+    T, N, K = 200, 70, 300
+    c, s, v = make_codes(gen, T, K, 1, E5, E8)
+    g = rand(gen, T, N, dtype=g_t)
+    g[3, 5], g[70, 6], g[150, 7], g[199, 8] = INF, math.nan, -INF, math.nan
+    if g_t == SF:  # the first part of a NaN has to be one
+        g.view(torch.int32)[70, 6] = 0x7F800001
+    c.view(torch.uint8)[80, 290] = 0x7C
+    v[80, 290] = INF
+    s.view(torch.uint8)[90, 1] = 255
+    v[90, 128:256] = math.nan
+    c.view(torch.uint8)[198, :] = 0x7F
+    s.view(torch.uint8)[197, :] = 255
+    y = fw.block_weight_grad(g.to(dev), c.to(dev), s.to(dev), torch.tensor([60, 120, 190], device=dev), out_dtype=SF).cpu()
+    for i, (a, b) in enumerate(((0, 60), (60, 120), (120, 190))):
+        h, x = g[a:b].to(f64), v[a:b]
+        want = h.t() @ x
+        size = h.abs().nan_to_num(0, 0, 0).t() @ x.abs().nan_to_num(0, 0, 0)
+        if g_t != BF:
+            # an infinity's other parts are 0: they meet an infinite code as 0 times infinity only where both are in one row
+            assert not (h.isinf().any(1) & x.isinf().any(1)).any()
+        close(y[i], want, size * F, "weights' gradient")
+    dense = fw.block_weight_grad(g.to(dev)[:190], c.to(dev)[:190], s.to(dev)[:190], out_dtype=SF).cpu()
+    assert dense[:, 128:256].isnan().all() and dense[6].isnan().all() and not dense[9, :128].isnan().any()
+
+
+@pytest.mark.gpu
+def test_weight_grad_of_far_scales_and_axes(dev):
+    """Scales over the whole of bf16's range; leading axes; no groups at all."""
+    gen = rng(6)
+    e = torch.randint(-100, 100, (64, 1), generator=gen)
+    c, s, v = exact_codes(gen, 64, 256, 1, E4, E8)
+    s = torch.exp2(e.float()).expand(64, 2).contiguous().to(E8)
+    v = c.to(f64) * torch.exp2(e.to(f64))
+    g = torch.zeros(64, 64)
+    g.fill_diagonal_(1.5)
+    y = fw.block_weight_grad(g.bfloat16().to(dev), c.to(dev), s.to(dev), out_dtype=SF)
+    assert torch.equal(y.cpu().to(f64), v * 1.5)
+    z = fw.block_weight_grad(g.bfloat16().to(dev).view(4, 16, 64), c.to(dev).view(4, 16, 256), s.to(dev).view(4, 16, 2), out_dtype=SF)
+    assert torch.equal(z, y)
+    assert fw.block_weight_grad(g.to(dev), c.to(dev), s.to(dev), torch.empty(0, dtype=torch.int64, device=dev)).shape == (0, 64, 256)
+    assert fw.block_weight_grad(g.to(dev)[:, :0], c.to(dev), s.to(dev)).shape == (0, 256)
+
+
 # ---- refusals (no GPU) ---------------------------------------------------------
 def c_quant(**kw):
     a = dict(x=16, xd=0, ldx=64, xs=0, E=1, T=2, n=64, rows=1, q=16, qd=3, s=16, sd=1)
@@ -676,6 +799,25 @@ def test_grouped_refusals(kw, status):
     assert c_grouped(**kw) == status
 
 
+def c_weight_grad(**kw):
+    a = dict(g=16, gd=0, ldg=64, c=16, cd=3, ldc=256, s=16, sr=2, sb=1, T=100, N=64, K=256, ends=None, bits=32, E=0, out=16, od=0,
+             ldo=256, os=64 * 256, ws=16, wsb=1 << 30)
+    a.update(kw)
+    return block_operators._lib().emu_block_weight_grad(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(T=-1), 1), (dict(N=-1), 1), (dict(K=-1), 1), (dict(E=-1), 1), (dict(gd=3), 1), (dict(cd=5), 1), (dict(od=4), 1),
+    (dict(E=2), 1), (dict(ends=16, E=2, bits=16), 1), (dict(ends=18, E=2), 1), (dict(g=None), 1), (dict(c=None), 1), (dict(s=None), 1),
+    (dict(out=None), 1), (dict(ldg=63), 1), (dict(ldc=255), 1), (dict(ldo=255), 1), (dict(ends=16, E=2, os=-1), 1),
+    (dict(ends=16, E=2, os=0), 1), (dict(g=17), 1), (dict(out=17), 1), (dict(sr=-1), 1), (dict(sb=-1), 1), (dict(ws=8), 1),
+    (dict(ldg=65, wsb=64), 4), (dict(c=17, wsb=64), 4), (dict(gd=2, ws=None), 4), (dict(T=2 ** 30 + 1), 3),
+    (dict(N=2 ** 22 + 1, ldg=2 ** 23), 3), (dict(K=2 ** 22 + 1, ldc=2 ** 23), 3), (dict(ends=16, E=65537), 3),
+    (dict(N=2 ** 20, K=2 ** 18, ldg=2 ** 20, ldc=2 ** 18, ldo=2 ** 18), 3), (dict(N=0), 0), (dict(K=0), 0), (dict(ends=16, E=0), 0)])
+def test_weight_grad_refusals(kw, status):
+    assert c_weight_grad(**kw) == status
+
+
 def test_product_workspaces():
     """Nothing where operands are aligned and K is not split; sizes that a call refuses need none."""
     lib = block_operators._lib()
@@ -701,6 +843,8 @@ def test_host_tensors_are_refused():
         fw.block_scaled_mm(q, q.t(), s, s[:1].t())
     with pytest.raises(ValueError):
         fw.grouped_block_scaled_mm(q, q[None].transpose(1, 2), s, s[None, :1].transpose(1, 2), torch.tensor([2]))
+    with pytest.raises(ValueError):
+        fw.block_weight_grad(x, q, s.to(E8))
     with pytest.raises(TypeError):
         fw.block_scaled_mm(x, q.t(), s, s[:1].t())
 
@@ -751,6 +895,20 @@ def test_product_binding_refusals(dev):
     for bad in (lambda: mm(q, W[0], s, t[0].t(), out_dtype=E4), lambda: gm(q, W, s, S, ends, out_dtype=I8)):
         with pytest.raises(fw.EmuError):
             bad()
+    g, wg = torch.zeros(40, 64, device=dev), fw.block_weight_grad
+    for bad in (lambda: wg(g[:39], q, s), lambda: wg(g, q, s[:39]), lambda: wg(g, q, s, ends[None]), lambda: wg(g, q, s, ends.cpu()),
+                lambda: wg(g.t(), q, s), lambda: wg(g, q, s, out=torch.zeros(64, 255, device=dev)), lambda: wg(g[0], q[0], s[0]),
+                lambda: wg(g, q, s, out=torch.zeros(256, 64, device=dev).t()), lambda: wg(g, q, s, ends[::2].expand(3))):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: wg(g.double(), q, s), lambda: wg(g, g, s), lambda: wg(g, q, s.float()), lambda: wg(g, q, s, ends.float()),
+                lambda: wg(g, q, s, out=torch.zeros(64, 256, dtype=BF, device=dev))):
+        with pytest.raises(TypeError):
+            bad()
+    with pytest.raises(fw.EmuError):
+        wg(g, q, s, out_dtype=E4)
+    with pytest.raises(RuntimeError):
+        wg(g.clone().requires_grad_(), q, s)
     b = torch.zeros(64, device=dev, requires_grad=True)
     with pytest.raises(RuntimeError):
         mm(q, W[0], s, t[0].t(), bias=b)
