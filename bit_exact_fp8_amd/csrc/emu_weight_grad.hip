@@ -122,16 +122,12 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void grad_tiles(WeightGradParams p,
     __shared__ __attribute__((aligned(1024))) int8_t lds[kGradLds<BN, BK>];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
-    // the tile: each XCD gets a run of them
-    int e, ti, tj;
-    {
-        const int per = tn * tk, total = (int)gridDim.x, xcd = (int)blockIdx.x & 7, each = total >> 3, rest = total & 7;
-        const int id = xcd * each + (xcd < rest ? xcd : rest) + ((int)blockIdx.x >> 3);
-        e = id / per;
-        const int in = id - e * per, pair = in / (2 * tk), high = tn - 2 * pair < 2 ? 1 : 2, at = in - pair * 2 * tk;
-        ti = 2 * pair + at % high;
-        tj = at / high;
-    }
+    // Groups one after the other, each one's tiles over all XCDs: groups differ
+    // in rows, and with one to an XCD the largest would end last (16384 x 8192 x
+    // 4096 in 8 groups as routers leave them: 1.99 ms).
+    const int e = (int)blockIdx.x / (tn * tk);
+    int ti, tj;
+    tile_of((int)blockIdx.x - e * (tn * tk), tn, tk, ti, tj);
     // the group's rows: an end below one before counts as that one, one past T as T
     int first = 0, rows = (int)p.T;
     if (p.E) {
