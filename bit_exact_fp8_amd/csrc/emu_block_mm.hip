@@ -228,11 +228,29 @@ __device__ __forceinline__ Scale<MODE> scale_from(uint32_t word, int e8m0)
 
 constexpr int kFar = (int)0x80000000;  // an offset past every range
 
+// Loads of a wave straight into LDS: 16 codes a lane, zeros from `size` bytes
+// on, and a scale a lane, a byte as a word.
+__device__ __forceinline__ void load_codes(const int8_t *base, int size, int offset, int8_t *to)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(__builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t *>(base), 0, size, 0x00020000),
+                                             (lds_ptr)to, 16, offset, 0, 0, 0);
+}
+__device__ __forceinline__ void load_byte(const char *base, int offset, uint32_t *to)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(__builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(base), 0, -1, 0x00020000),
+                                             (lds_ptr)to, 1, offset, 0, 0, 0);
+}
+__device__ __forceinline__ void load_word(const char *base, int offset, uint32_t *to)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(__builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(base), 0, -1, 0x00020000),
+                                             (lds_ptr)to, 4, offset, 0, 0, 0);
+}
+
 template <int MODE, int BM, int BN, int WM, int WN, int NB>
 struct TileShape {
     static constexpr int FM = BM / WM / 16, FN = BN / WN / 16;  // a wave's fragments
     static constexpr int threads = WM * WN * 64;
-    static constexpr int LPW = (BM + BN) / 8 / (WM * WN);       // its loads a stage, 8 rows each
+    static constexpr int LA = BM / 8 / (WM * WN), LW = BN / 8 / (WM * WN);  // its loads of a and of w a stage, 8 rows each
     static constexpr int BUF = (BM + BN) * kStage;
     static constexpr int RA = FM < 4 ? FM : 4;                  // fragments of a held in registers
     static constexpr int TAIL = MODE == kExact ? 0 : FM >= 4 ? 2 : 1;
@@ -244,8 +262,8 @@ __global__ __launch_bounds__(WM * WN * 64, (TileShape<MODE, BM, BN, WM, WN, NB>:
     BlockMMParams p, int tm, int tn, int stages, float *part)
 {
     typedef TileShape<MODE, BM, BN, WM, WN, NB> S;
-    constexpr int FM = S::FM, FN = S::FN, LPW = S::LPW, BUF = S::BUF, RA = S::RA, TAIL = S::TAIL, L = LPW + 1, T = FM * FN;
-    static_assert(LPW * WM * WN * 8 == BM + BN && BM % (LPW * 8) == 0 && LPW % 2 == 0 && FM % RA == 0, "a wave loads of one operand");
+    constexpr int FM = S::FM, FN = S::FN, LA = S::LA, LW = S::LW, BUF = S::BUF, RA = S::RA, TAIL = S::TAIL, L = LA + LW + 1, T = FM * FN;
+    static_assert(LA * WM * WN * 8 == BM && LW * WM * WN * 8 == BN && LA % 2 == 0 && LW % 2 == 0 && FM % RA == 0, "a wave's loads");
     static_assert(BM % 64 == 0 && BM + BN <= S::threads && 128 % (BN / WN) == 0, "a wave's scales");
     __shared__ __attribute__((aligned(1024))) int8_t lds[S::lds];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -256,7 +274,7 @@ __global__ __launch_bounds__(WM * WN * 64, (TileShape<MODE, BM, BN, WM, WN, NB>:
         const bool found = find_rows(p, lane, BM,
                                      [&](int total, int &t) {
                                          if ((int64_t)blockIdx.x >= (int64_t)total * tn) return false;
-                                         tile_of(blockIdx.x, total, tn, t, tj);
+                                         tile_of<kHigh>(blockIdx.x, total, tn, t, tj);
                                          return true;
                                      },
                                      at);
@@ -267,7 +285,7 @@ __global__ __launch_bounds__(WM * WN * 64, (TileShape<MODE, BM, BN, WM, WN, NB>:
         }
     } else {
         int ti;
-        tile_of(blockIdx.x, tm, tn, ti, tj);
+        tile_of<kHigh>(blockIdx.x, tm, tn, ti, tj);
         at = {(int64_t)ti * BM, p.M, 0};
     }
     const int64_t m0 = uniform(at.first), n0 = (int64_t)uniform(tj) * BN;
@@ -277,19 +295,18 @@ __global__ __launch_bounds__(WM * WN * 64, (TileShape<MODE, BM, BN, WM, WN, NB>:
     const int K = (int)(p.K - k0 < (int64_t)stages * kStage ? p.K - k0 : (int64_t)stages * kStage);
     const int count = (K + kStage - 1) / kStage;
 
-    // this wave's operand, and a lane's places in the first two of its loads
-    const bool of_w = wave * LPW * 8 >= BM;
-    const int64_t ld = of_w ? p.ldw : p.lda;
-    const int8_t *base = of_w ? p.w + at.e * p.w_stride + n0 * p.ldw + k0 : p.a + m0 * p.lda + k0;
-    const auto range = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t *>(base), 0,
-                                                         (int)(((of_w ? cols : rows) - 1) * ld) + K, 0x00020000);
-    const int row0 = wave * LPW * 8 - (of_w ? BM : 0) + (lane >> 3), ld8 = 8 * (int)ld;
-    int chunk[2], from[2];
-    chunk[0] = ((lane & 7) ^ swizzle(lane >> 3)) * 16;
-    chunk[1] = ((lane & 7) ^ swizzle(8 + (lane >> 3))) * 16;
-    from[0] = row0 * (int)ld + chunk[0];
-    from[1] = row0 * (int)ld + chunk[1];
-    int8_t *const dst = lds + wave * LPW * 1024;
+    // the operands, and a lane's places in the first two of this wave's loads of each
+    const int8_t *const base_a = p.a + m0 * p.lda + k0, *const base_w = p.w + at.e * p.w_stride + n0 * p.ldw + k0;
+    const int size_a = (rows - 1) * (int)p.lda + K, size_w = (cols - 1) * (int)p.ldw + K;
+    const int lda8 = 8 * (int)p.lda, ldw8 = 8 * (int)p.ldw;
+    int chunk[2], from_a[2], from_w[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        chunk[h] = ((lane & 7) ^ swizzle(h * 8 + (lane >> 3))) * 16;
+        from_a[h] = (wave * LA * 8 + (lane >> 3)) * (int)p.lda + chunk[h];
+        from_w[h] = (wave * LW * 8 + (lane >> 3)) * (int)p.ldw + chunk[h];
+    }
+    int8_t *const to_a = lds + wave * LA * 1024, *const to_w = lds + BM * kStage + wave * LW * 1024;
 
     // scales: a word for each of the tile's rows, then for each of its columns
     const int size = p.e8m0 ? 1 : 4;
@@ -307,19 +324,22 @@ __global__ __launch_bounds__(WM * WN * 64, (TileShape<MODE, BM, BN, WM, WN, NB>:
 
     // load q of stage s; `whole`: it lies within K
     const auto load = [&](int q, int s, int buf, bool whole) {
-        if (q == LPW) {
-            const auto r = __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(sbase) + (s < count ? s : count - 1) * sstep, 0, -1,
-                                                             0x00020000);
-            const lds_ptr to = (lds_ptr)(words + buf * S::threads + wave * 64);
+        if (q == LA + LW) {
+            const char *const from = sbase + (s < count ? s : count - 1) * sstep;
+            uint32_t *const to = words + buf * S::threads + wave * 64;
             if (MODE == kHardware || (MODE == kExact && p.e8m0))
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(r, to, 1, sfrom, 0, 0, 0);
+                load_byte(from, sfrom, to);
             else
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(r, to, 4, sfrom, 0, 0, 0);
+                load_word(from, sfrom, to);
             return;
         }
-        int off = from[q & 1] + q * ld8 + s * kStage;
-        if (!whole && s * kStage + chunk[q & 1] >= K) off = kFar;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(range, (lds_ptr)(dst + buf * BUF + q * 1024), 16, off, 0, 0, 0);
+        const int u = q < LA ? q : q - LA;
+        int off = (q < LA ? from_a[u & 1] + u * lda8 : from_w[u & 1] + u * ldw8) + s * kStage;
+        if (!whole && s * kStage + chunk[u & 1] >= K) off = kFar;
+        if (q < LA)
+            load_codes(base_a, size_a, off, to_a + buf * BUF + u * 1024);
+        else
+            load_codes(base_w, size_w, off, to_w + buf * BUF + u * 1024);
     };
 
     const int wm = (wave / WN) * (BM / WM), wn = (wave % WN) * (BN / WN), fr = lane & 15;
@@ -441,7 +461,7 @@ __global__ __launch_bounds__(WM * WN * 64, (TileShape<MODE, BM, BN, WM, WN, NB>:
 #pragma unroll
     for (int j = 0; j < FN; ++j) bias[j] = bias_at(p, n + j * 16);
     const bool whole = rows == BM && cols == BN;
-    store_tile(p.out, p.out_dtype, p.ldo, acc, p.bias ? bias : nullptr, m, at.end, n0 + wn, p.N, lane, whole);
+    store_tile(p.out, p.out_dtype, p.ldo, acc, bias, p.bias != nullptr, m, at.end, n0 + wn, p.N, lane, whole);
 }
 
 // ---- few rows --------------------------------------------------------------
@@ -590,7 +610,10 @@ void launch_mode(const BlockMMParams &p, const BlockPlan &plan, float *part, hip
     } else if (plan.tile == 1 || MODE == kExact) {
         launch_tiles<AF, WF, MODE, 128, 128, 2, 4, 2>(p, plan, part, stream);
     } else if constexpr (MODE != kExact) {
-        launch_tiles<AF, WF, MODE, 256, 256, 2, 4, 2>(p, plan, part, stream);
+        if (plan.tile == 2)
+            launch_tiles<AF, WF, MODE, 256, 128, 2, 4, 3>(p, plan, part, stream);
+        else
+            launch_tiles<AF, WF, MODE, 256, 256, 2, 4, 2>(p, plan, part, stream);
     }
 }
 

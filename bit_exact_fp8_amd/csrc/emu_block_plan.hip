@@ -60,12 +60,22 @@ __global__ __launch_bounds__(256) void block_join(BlockMMParams p, const float *
     });
 }
 
-// The tiles, with what one stage of a tile costs a CU in microseconds in each mode.
+// The tiles, with what the CUs take for a round of one tile each or (where LDS
+// has room for two) of two: microseconds to begin and end, and for each stage in
+// kHardware.  Measured at 4096 x 4096 of K with 128 to 2048 rows and at 8192^3.
 struct Tile {
-    int bm, bn;
-    double stage[3];
+    int bm, bn, per_cu;
+    double ends, stage, stage2;
 };
-constexpr Tile kTiles[] = {{64, 64, {0.20, 0.20, 0.25}}, {128, 128, {0.55, 0.55, 0.75}}, {256, 256, {1.60, 1.70, 0}}};
+constexpr Tile kTiles[] = {{64, 64, 2, 3.0, 0.28, 0.45}, {128, 128, 2, 4.0, 0.84, 1.25}, {256, 128, 1, 6.0, 1.02, 0}, {256, 256, 1, 12.0, 1.45, 0}};
+constexpr double kStageOf[] = {1.0, 1.1, 2.0};  // of each mode, relative to kHardware
+
+double tiles_us(const Tile &t, int64_t tiles, int64_t stages, int mode)
+{
+    const double one = t.ends + (double)stages * t.stage * kStageOf[mode], two = t.ends + (double)stages * t.stage2 * kStageOf[mode];
+    const int64_t round = 256 * t.per_cu, left = tiles % round;
+    return (double)(tiles / round) * (t.per_cu == 2 ? two : one) + (left == 0 ? 0.0 : left > 256 ? two : one);
+}
 
 struct Plan {
     BlockPlan kernel;
@@ -88,9 +98,10 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int E, bool grouped, int mode, b
     const int64_t total = blocks_of(K);
     k.stages = total ? (int)total : 1;
     const bool ra = needs_repack(K, a_aligned), rw = needs_repack(K, w_aligned);
-    // Few rows (of each group, in the mean) read w once and wait for nothing.
+    // Operands that are not aligned are laid out anew for tiles, which for up to
+    // 64 rows (of each group, in the mean) takes longer than to read them in words.
     const int64_t mean = mean_rows(M, E, grouped);
-    if (mean <= 32 || (mean <= 64 && (ra || rw)) || K == 0) {
+    if ((mean <= 64 && (ra || rw)) || K == 0) {
         k.rows = mean <= 16 || K == 0 ? 1 : mean <= 32 ? 2 : 4;
         k.waves = k.rows == 4 ? 8 : K > 4096 ? (k.rows == 1 ? 16 : 8) : 4;
         return p;
@@ -100,24 +111,31 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int E, bool grouped, int mode, b
     p.ld = total * kStage;
     p.a_bytes = ra ? M * p.ld : 0;
     p.w_bytes = rw ? (int64_t)E * N * p.ld : 0;
-    // The fastest estimate: 1 us and its stages for each round of 256 tiles
-    // (one for a CU), and for a split of K 5 us and its sums at 4 TB/s, there
-    // and back.  Each group's last tile is half full in the mean.
+    // The fastest estimate; a split of K takes 5 us more and its sums at 4 TB/s,
+    // there and back.  Each group's last tile is half full in the mean.
     double best = 0.0;
-    for (int i = 0; i < (mode == kExact ? 2 : 3); ++i)
+    for (int i = 0; i < (mode == kExact ? 2 : 4); ++i)
         for (int S = 1; S <= (grouped ? 1 : 8); S *= 2) {
             const int64_t stages = ceil_div(total, S);
             if (S > 1 && stages < 4) break;
-            const int64_t tm = grouped ? M / kTiles[i].bm + (E < M ? E : M) / 2 + 1 : ceil_div(M, kTiles[i].bm);
-            const int64_t tiles = tm * ceil_div(N, kTiles[i].bn);
-            const double rounds = (double)ceil_div(tiles * S, 256);
-            double us = rounds * (1.0 + (double)stages * kTiles[i].stage[mode]);
+            const int64_t tm = grouped ? ceil_div(M, kTiles[i].bm) + (E < M ? E : M) / 2 : ceil_div(M, kTiles[i].bm);
+            double us = tiles_us(kTiles[i], tm * ceil_div(N, kTiles[i].bn) * S, stages, mode);
             if (S > 1) us += 5.0 + (double)S * (double)M * (double)N * 8.0 / 4e6;
             if (k.tile >= 0 && us >= best) continue;
             best = us;
             k.tile = i;
             k.S = S;
         }
+    // Up to 16 rows read w once, straight into registers, and wait for nothing,
+    // but read a again for every 16 columns (16 x 4096 x 4096: 10.0 us, in tiles
+    // 11.2; 16 x 8192 x 8192: 24.2 and 16.7).  Groups take tiles in any case: 32 x
+    // 4096 x 2048 over 16 of them 29.9 us, in tiles 26.4.
+    if (!grouped && M <= 16 && 2.5 + (double)N * (double)K * (1.0 + (double)M / 16.0) / 7.5e6 < best) {
+        k.tile = -1;
+        k.S = k.rows = 1;
+        k.waves = K > 4096 ? 16 : 4;
+        return p;
+    }
     k.stages = total ? (int)ceil_div(total, k.S) : 1;
     k.S = total ? (int)ceil_div(total, k.stages) : 1;
     p.part_bytes = k.S > 1 ? k.S * M * N * 4 : 0;

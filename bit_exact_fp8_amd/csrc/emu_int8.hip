@@ -115,7 +115,7 @@ __global__ __launch_bounds__(WM * WN * 64, NB * (BM + BN) * kStage * 2 <= 160 * 
     __shared__ __attribute__((aligned(1024))) int8_t lds[NB * BUF];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int ti, tj;
-    tile_of(blockIdx.x, tm, tn, ti, tj);
+    tile_of<2>(blockIdx.x, tm, tn, ti, tj);
     const int64_t m0 = (int64_t)ti * BM, n0 = (int64_t)tj * BN;
     const int64_t k0 = (int64_t)blockIdx.y * stages * kStage;     // this split's first code
     const int K = (int)(p.K - k0 < (int64_t)stages * kStage ? p.K - k0 : (int64_t)stages * kStage);

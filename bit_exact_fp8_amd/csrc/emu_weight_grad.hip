@@ -127,7 +127,7 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void grad_tiles(WeightGradParams p,
     // 4096 in 8 groups as routers leave them: 1.99 ms).
     const int e = (int)blockIdx.x / (tn * tk);
     int ti, tj;
-    tile_of((int)blockIdx.x - e * (tn * tk), tn, tk, ti, tj);
+    tile_of<kHigh>((int)blockIdx.x - e * (tn * tk), tn, tk, ti, tj);
     // the group's rows: an end below one before counts as that one, one past T as T
     int first = 0, rows = (int)p.T;
     if (p.E) {
@@ -285,13 +285,13 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void grad_tiles(WeightGradParams p,
     }
     const int64_t n = n0 + wn + (lane & 15);
     const bool whole = cols_n == BN && cols_k == BK;
+    const f32x4 none[FK] = {};
     if (part)
-        store_tile(part + ((int64_t)blockIdx.y * (p.E ? p.E : 1) + e) * p.N * p.K, EMU_DT_FP32, p.K, acc, nullptr, n, p.N, k0 + wk, p.K,
+        store_tile(part + ((int64_t)blockIdx.y * (p.E ? p.E : 1) + e) * p.N * p.K, EMU_DT_FP32, p.K, acc, none, false, n, p.N, k0 + wk, p.K,
                    lane, whole);
-    else if (p.out_dtype == EMU_DT_FP32)
-        store_tile(static_cast<float *>(p.out) + e * p.out_stride, p.out_dtype, p.ldo, acc, nullptr, n, p.N, k0 + wk, p.K, lane, whole);
     else
-        store_tile(static_cast<uint16_t *>(p.out) + e * p.out_stride, p.out_dtype, p.ldo, acc, nullptr, n, p.N, k0 + wk, p.K, lane, whole);
+        store_tile(static_cast<char *>(p.out) + e * p.out_stride * (p.out_dtype == EMU_DT_FP32 ? 4 : 2), p.out_dtype, p.ldo, acc, none,
+                   false, n, p.N, k0 + wk, p.K, lane, whole);
 }
 
 // The sums of S splits, four outputs a thread.

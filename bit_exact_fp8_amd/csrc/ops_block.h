@@ -116,6 +116,12 @@ void launch_block_kernel(const BlockMMParams &p, const BlockPlan &plan, float *p
 
 #ifdef __HIPCC__
 
+// Rows of tiles that an XCD's run is high: with 4 its 32 tiles at a time read 12
+// tiles' worth of operands, with 2 18 (the product of 16384 x 8192 x 4096: 408 us
+// and 425, in 8 groups 495 and 529, its weights' gradient 986 and 1003; with 8 469,
+// 500 and 986).
+constexpr int kHigh = 4;
+
 // The value of a scale byte: 2^(b - 127) (a subnormal number for 0), NaN for 255.
 __device__ __forceinline__ float e8m0_value(uint32_t b)
 {

@@ -71,14 +71,15 @@ __device__ __forceinline__ void wait_loads()
 
 typedef __attribute__((address_space(3))) void *lds_ptr;
 
-// Workgroups go round the 8 XCDs in turn; each XCD gets a run of
-// neighbouring tiles, two rows of tiles high, whose operands its L2 then holds.
+// Workgroups go round the 8 XCDs in turn; each XCD gets a run of neighbouring
+// tiles, HIGH rows of tiles high, whose operands its L2 then holds.
+template <int HIGH>
 __device__ __forceinline__ void tile_of(int id, int tm, int tn, int &m, int &n)
 {
     const int total = tm * tn, xcd = id & 7, each = total >> 3, rest = total & 7;
     id = xcd * each + (xcd < rest ? xcd : rest) + (id >> 3);
-    const int pair = id / (2 * tn), high = tm - 2 * pair < 2 ? 1 : 2, in = id - pair * 2 * tn;
-    m = 2 * pair + in % high;
+    const int band = id / (HIGH * tn), left = tm - HIGH * band, high = left < HIGH ? left : HIGH, in = id - band * HIGH * tn;
+    m = HIGH * band + in % high;
     n = in / high;
 }
 
@@ -140,12 +141,12 @@ __device__ __forceinline__ i32x4 load16(const int8_t *row, int64_t k, int64_t K)
 
 // A wave's outputs: fragment (i, j) holds the outputs of row m + 16 i from
 // column n + 16 j + 4 (lane / 16) on, four to a lane; `whole`: all of them lie
-// within the matrix.  Outputs of 16 bits go out eight to a lane: the quarters of
+// within the matrix; `add`: a bias for each column.  Outputs of 16 bits go out eight to a lane: the quarters of
 // a wave swap halves between two fragments, and a store then writes 64 bytes
 // of each of 16 rows, not 32.
 template <int FM, int FN>
-__device__ __forceinline__ void store_tile(void *to, int dtype, int64_t ld, const f32x4 (&acc)[FM][FN], const f32x4 *bias, int64_t m,
-                                           int64_t rows, int64_t n, int64_t cols, int lane, bool whole)
+__device__ __forceinline__ void store_tile(void *to, int dtype, int64_t ld, const f32x4 (&acc)[FM][FN], const f32x4 (&bias)[FN], bool add,
+                                           int64_t m, int64_t rows, int64_t n, int64_t cols, int lane, bool whole)
 {
     with_type(dtype, [&](auto *type) {
         typedef std::remove_pointer_t<decltype(type)> E;
@@ -158,7 +159,7 @@ __device__ __forceinline__ void store_tile(void *to, int dtype, int64_t ld, cons
 #pragma unroll
             for (int j = 0; j < FN; j += 2) {
                 f32x4 x = acc[i][j], y = acc[i][j + 1];
-                if (bias) x += bias[j], y += bias[j + 1];
+                if (add) x += bias[j], y += bias[j + 1];
                 const Four<E> v = __builtin_convertvector(x, Four<E>), w = __builtin_convertvector(y, Four<E>);
                 if constexpr (sizeof(E) == 2) {
                     typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
