@@ -524,6 +524,13 @@ void dense(const char *name, const Tensor &t, at::IntArrayRef shape, c10::Device
     shaped(name, t, shape, device);
     if (!t.is_contiguous()) value_error(std::string(name) + " must be dense");
 }
+// A gradient, laid out where it is one value (or row) expanded.
+Tensor laid_out(const Tensor &t)
+{
+    for (int64_t d = 0; d < t.dim(); ++d)
+        if (t.stride(d) == 0 && t.size(d) > 1) return t.contiguous();
+    return t;
+}
 bool truth(PyObject *o)
 {
     const int b = PyObject_IsTrue(o);
@@ -609,8 +616,9 @@ PyObject *swiglu_block_quant(PyObject *const *a)
 PyObject *swiglu_block_backward(PyObject *const *a)
 {
     outside_autograd({a[0], a[1], a[2]});
-    const Tensor &g = gpu("grad_h", a[0]), &kept = tensor("kept", a[1]), &kept_s = tensor("kept_scale", a[2]);
-    floating("grad_h", g);
+    const Tensor &given = gpu("grad_h", a[0]), &kept = tensor("kept", a[1]), &kept_s = tensor("kept_scale", a[2]);
+    floating("grad_h", given);
+    const Tensor g = laid_out(given);
     codes("kept", kept);
     scales("kept_scale", kept_s);
     const Rows r = rows("grad_h", g);
@@ -751,9 +759,10 @@ PyObject *grouped_block_scaled_mm(PyObject *const *a)
 PyObject *block_weight_grad(PyObject *const *a)
 {
     outside_autograd({a[0], a[1], a[2]}, {a[5]});
-    const Tensor &g = gpu("grad", a[0]), &x = tensor("codes", a[1]), &s = tensor("scale", a[2]);
+    const Tensor &grad = gpu("grad", a[0]), &x = tensor("codes", a[1]), &s = tensor("scale", a[2]);
     const Tensor *ends = optional("ends", a[3]), *given = optional("out", a[5]);
-    floating("grad", g);
+    floating("grad", grad);
+    const Tensor g = laid_out(grad);
     codes("codes", x);
     if (s.scalar_type() != ScalarType::Float8_e8m0fnu)
         type_error("scale must be float8_e8m0fnu (powers of two), not " + str(s.scalar_type()));

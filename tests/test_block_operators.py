@@ -715,6 +715,160 @@ def test_weight_grad_of_far_scales_and_axes(dev):
     assert fw.block_weight_grad(g.to(dev)[:, :0], c.to(dev), s.to(dev)).shape == (0, 256)
 
 
+# ---- all of them together ---------------------------------------------------------
+def values(codes, scale, rows=1):
+    """What codes and scales on the device stand for, in 64 bits on the host."""
+    c, s = codes.cpu().float().to(f64), scale.cpu().float().to(f64)
+    T, n = c.shape[-2:]
+    return c * spread(s, T, n, rows)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,n,hidden,E,c", [(1, 128, 64, 3, 1), (33, 200, 130, 4, 2), (150, 256, 128, 9, 3)])
+def test_expert_step(dev, T, n, hidden, E, c):
+    """A layer of experts forward and back: each product against the same in 64
+    bits on the codes that the step has, its sums over choices and places too."""
+    from bit_exact_fp8_amd import expert_step as es
+    note(f"expert step T={T} n={n} F={hidden} E={E} c={c}")
+    gen = rng(T)
+    up, down = es.project(rand(gen, E, 2 * hidden, n, std=n ** -0.5).to(dev)), es.project(rand(gen, E, n, hidden, std=0.1).to(dev))
+    x, grad = rand(gen, T, n, dtype=BF), rand(gen, T, n, dtype=BF)
+    choice = torch.stack([torch.randperm(E, generator=gen)[:c] for _ in range(T)])
+    choice[choice == 1] = 0  # (an expert without a row)
+    share = torch.rand(T, c, generator=gen)
+    out, kept = es.forward(x.to(dev), up, down, choice.to(dev), share.to(dev))
+    g = es.backward(grad.to(dev), kept, up, down, share.to(dev))
+    order, ends = kept.order.cpu(), kept.ends.cpu().tolist()
+    token = order // c
+    assert torch.equal(choice.reshape(-1)[order].sort().values, choice.reshape(-1)[order]) and ends[-1] == T * c
+    same(kept.x, quant64(x[token], 1, E4, E8)[0], "rows' codes")
+    xv, hv = values(kept.x, kept.x_scale), values(kept.h.codes, kept.h.scale)
+    w_up, w_down = values(up.codes, up.scale, 128), values(down.codes, down.scale, 128)
+    assert torch.equal(values(up.turned, up.turned_scale, 128), w_up.transpose(1, 2))
+    part = share.reshape(-1)[order, None].to(f64)
+    rows = (grad.float()[token] * part.float()).to(BF)
+    rq, rs = quant64(rows, 1, E4, E8)
+    rv = rq * spread(rs, T * c, n, 1)
+    y, y_tol = torch.zeros(T * c, n, dtype=f64), torch.zeros(T * c, n, dtype=f64)
+    both, both_tol = torch.zeros(T * c, 2 * hidden, dtype=f64), torch.zeros(T * c, 2 * hidden, dtype=f64)
+    gh, gh_tol = torch.zeros(T * c, hidden, dtype=f64), torch.zeros(T * c, hidden, dtype=f64)
+    for e, (a, b) in enumerate(spans(ends, T * c)):
+        for v, wv, to, tol, t in ((xv, w_up[e], both, both_tol, BF), (hv, w_down[e], y, y_tol, SF),
+                                  (rv, w_down[e].t().contiguous(), gh, gh_tol, BF)):
+            to[a:b] = v[a:b] @ wv.t()
+            tol[a:b] = mm_bound(v[a:b], wv, to[a:b], t)
+        want = rows[a:b].to(f64).t() @ hv[a:b]
+        close(g.down[e], want, half_step(want, SF) + F * (rows[a:b].to(f64).abs().t() @ hv[a:b].abs()), "down's gradient")
+    # what was kept of gate and up is a rounding of the product: half a step of the codes, or the product's own error
+    k = blocks(hidden)
+    for i in range(2):
+        v = both[:, i * hidden:(i + 1) * hidden]
+        s = spread(kept.h.kept_scale.cpu().float().to(f64)[:, i * k:(i + 1) * k], T * c, hidden, 1)
+        z = kept.h.kept.cpu().float().to(f64)[:, i * hidden:(i + 1) * hidden]
+        tol = both_tol[:, i * hidden:(i + 1) * hidden]
+        # (a step of codes at the value, which the product's error moves by less than one more of them)
+        assert bool(((z * s - v).abs() <= tol * 1.1 + (half_step(v / s, E4) + half_step(z, E4)) * s).all())
+    want = torch.zeros(T, n, dtype=f64).index_add_(0, token, y * part)
+    tol = torch.zeros(T, n, dtype=f64).index_add_(0, token, y_tol * part + F * (y * part).abs())
+    close(out, want, half_step(want, BF) + tol * 1.01, "output")
+    a, b = kept_values(kept.h.kept, kept.h.kept_scale, hidden)
+    p, q = torch.sigmoid(a), torch.sigmoid(-a)
+    d_gate, d_up = (b * p * (1 + a * q)), a * p
+    gb = torch.cat([gh * d_gate, gh * d_up], 1)
+    gb_tol = torch.cat([gh_tol * d_gate.abs() + F * gh.abs() * (b * p).abs() * (1 + (a * q).abs()), gh_tol * d_up.abs() + F * gb[:, hidden:].abs()], 1)
+    gb_tol = gb_tol * 1.01 + half_step(gb, BF)
+    for e, (i, j) in enumerate(spans(ends, T * c)):
+        want = gb[i:j].t() @ xv[i:j]
+        close(g.up[e], want, half_step(want, SF) + (gb_tol[i:j].t() @ xv[i:j].abs()) * 1.01 + F * (gb[i:j].abs().t() @ xv[i:j].abs()), "up's gradient")
+    # the input's gradient goes through codes of gb: half a step of each block's own scale, of the bounds' size
+    m = torch.nn.functional.pad(gb.abs() + gb_tol, (0, -2 * hidden % 128)).unflatten(1, (-1, 128)).amax(2)
+    s = spread(scale64(m.float().to(f64), E4, E8), T * c, 2 * hidden, 1)
+    code_tol = gb_tol + half_step((gb.abs() + gb_tol) / s, E4) * s
+    gx, gx_tol = torch.zeros(T * c, n, dtype=f64), torch.zeros(T * c, n, dtype=f64)
+    for e, (i, j) in enumerate(spans(ends, T * c)):
+        gx[i:j] = gb[i:j] @ w_up[e]
+        gx_tol[i:j] = code_tol[i:j] @ w_up[e].abs() + F * (gb[i:j].abs() @ w_up[e].abs())
+    want = torch.zeros(T, n, dtype=f64).index_add_(0, token, gx)
+    tol = torch.zeros(T, n, dtype=f64).index_add_(0, token, gx_tol * 1.01 + F * gx.abs())
+    close(g.x, want, half_step(want, BF) + tol, "input's gradient")
+
+
+@pytest.mark.gpu
+def test_expert_step_runs(dev):
+    from bit_exact_fp8_amd import expert_step as es
+    for experts in (1, 5):
+        assert math.isfinite(es.main(["--experts", str(experts), "--steps", "2", "--tokens", "70"]))
+
+
+@pytest.mark.gpu
+def test_block_operators_on_another_stream_and_in_a_graph(dev):
+    """The same bits on another stream, and on every replay of a captured chain,
+    with eager work between the replays and other ends in the captured call's tensor."""
+    gen = rng(9)
+    x, w = rand(gen, 300, 520, dtype=BF).to(dev), rand(gen, 4, 512, 520, std=0.05).to(dev)
+    w2 = rand(gen, 4, 333, 256, std=0.05).to(dev)
+    g = rand(gen, 300, 333).to(dev)
+    ends = torch.tensor([100, 100, 250, 290], device=dev)
+
+    def chain():
+        q, s = fw.block_quant(x)
+        wq, ws = fw.block_quant(w, block_rows=128)
+        both = fw.grouped_block_scaled_mm(q, wq.transpose(1, 2), s, ws.transpose(1, 2), ends)
+        h = fw.swiglu_block_quant(both[:, :256], both[:, 256:], keep=True)
+        wq2, ws2 = fw.block_quant(w2, block_rows=128)
+        y = fw.block_scaled_mm(h.codes, wq2[0].t(), h.scale, ws2[0].t(), out_dtype=SF)
+        d2 = fw.block_weight_grad(g, h.codes, h.scale, ends)
+        gh = fw.swiglu_block_backward(both[:, :256], h.kept, h.kept_scale)
+        d1 = fw.block_weight_grad(gh, q, s, ends, out_dtype=SF)
+        return [q.float(), s.float(), both, h.codes.float(), h.kept.float(), y, d2, gh, d1]
+
+    eager = [t.clone() for t in chain()]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = chain()
+        chain()
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(eager, other))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = chain()
+    for i in range(4):
+        ends.copy_(torch.tensor([100, 100, 250, 290] if i % 2 == 0 else [0, 30, 30, 300], device=dev))
+        want = [t.clone() for t in chain()]
+        for t in held:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize(dev)
+        assert all(torch.equal(a, b) for a, b in zip(want, held)), f"replay {i}"
+        assert i % 2 or all(torch.equal(a, b) for a, b in zip(eager, held))
+
+
+@pytest.mark.gpu
+def test_broadcast_gradients(dev):
+    """Expanded gradients, as a sum's or a mean's gradient is one."""
+    gen = rng(8)
+    q, s = fw.block_quant(rand(gen, 40, 200, dtype=BF).to(dev))
+    r = fw.swiglu_block_quant(rand(gen, 40, 200).to(dev), rand(gen, 40, 200).to(dev), keep=True)
+    one, row = torch.ones(1, 1, device=dev), rand(gen, 1, 200).to(dev)
+    for a in (one.expand(40, 200), row.expand(40, 200), row.t().contiguous()[:40].expand(40, 200)):
+        assert torch.equal(fw.block_weight_grad(a, q, s), fw.block_weight_grad(a.contiguous(), q, s))
+        assert torch.equal(fw.swiglu_block_backward(a, r.kept, r.kept_scale), fw.swiglu_block_backward(a.contiguous(), r.kept, r.kept_scale))
+
+
+@pytest.mark.gpu
+def test_block_outputs_count_a_version(dev):
+    q, s = fw.block_quant(torch.ones(64, 128, device=dev))
+    w, t = fw.block_quant(torch.ones(1, 32, 128, device=dev), block_rows=128)
+    ends = torch.tensor([64], device=dev)
+    out, wide_out = torch.zeros(64, 32, dtype=BF, device=dev), torch.zeros(1, 32, 128, device=dev)
+    for o, call in ((out, lambda: fw.block_scaled_mm(q, w[0].t(), s, t[0].t(), out=out)),
+                    (out, lambda: fw.grouped_block_scaled_mm(q, w.transpose(1, 2), s, t.transpose(1, 2), ends, out=out)),
+                    (wide_out, lambda: fw.block_weight_grad(torch.ones(64, 32, device=dev), q, s, ends, out=wide_out))):
+        version = o._version
+        assert call() is o and o._version == version + 1
+
+
 # ---- refusals (no GPU) ---------------------------------------------------------
 def c_quant(**kw):
     a = dict(x=16, xd=0, ldx=64, xs=0, E=1, T=2, n=64, rows=1, q=16, qd=3, s=16, sd=1)
