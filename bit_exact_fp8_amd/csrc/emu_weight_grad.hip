@@ -59,10 +59,14 @@ __global__ __launch_bounds__(256) void split_planes(const G *g, int64_t ldg, int
 // and ds_read_b64_tr_b16 turns 4 rows by 16 columns as it reads them, so that a
 // lane gets consecutive rows of its column.  While a half is multiplied out of
 // registers the next is read:
-//   (s, 0): multiply; read the fragments of (s, 1);
+//   (s, 0): multiply; read the fragments of (s, 1), write the codes of s + 1 into
+//           the other buffer and load those of s + 2;
 //   wait until every wave has written s + 1 and read buffer s (one barrier a stage);
-//   (s, 1): multiply; read the fragments of (s + 1, 0), write s + 2 into buffer s and
-//           load s + 3.
+//   (s, 1): multiply; read the fragments of (s + 1, 0), write g of s + 2 into buffer
+//           s and load that of s + 3.
+// LDS bounds it: a stage of 64 rows writes 64 KiB and reads 192 to 2048 cycles of
+// products, and 16384 x 8192 x 4096 in 8 groups (920 us) takes 750 without the
+// writes and 820 without the reads.  With both operands' writes in one half, 936.
 // (Loads straight into LDS would spare g its way through registers, but the
 // compiler then waits for all of them before each read that turns: 2.4 ms for 1.2.)
 // 16 rows' segments of 32 bytes meet in one read: row t's pair of chunks of 16
@@ -110,7 +114,10 @@ __device__ __forceinline__ s16x4 read_turned(const int8_t *lds)
 }
 
 // part: null, or [S, E, N, K] sums of each split of a group's rows (grid y).
-template <int CF, int BN, int BK, int WN, int WK>
+// PLANES: g may have more planes than one (without the test in the writes, one
+// plane of 16384 x 8192 x 4096 in 8 groups takes 945 us for 976, 1024 x 1920 x
+// 1920 21.0 for 23.0).
+template <int CF, bool PLANES, int BN, int BK, int WN, int WK>
 __global__ __launch_bounds__(WN *WK * 64, 2) void grad_tiles(WeightGradParams p, int tn, int tk, int S,
                                                                                                 float *part)
 {
@@ -147,7 +154,7 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void grad_tiles(WeightGradParams p,
     const int64_t n0 = (int64_t)ti * BN, k0 = (int64_t)tj * BK;
     const int cols_n = (int)(p.N - n0 < BN ? p.N - n0 : BN), cols_k = (int)(p.K - k0 < BK ? p.K - k0 : BK);
     // this split's stages: of all of the group's, plane after plane
-    const int per_plane = (int)(((unsigned)rows + kRows - 1) / kRows), all = per_plane * p.planes, share = uniform((all + S - 1) / S);
+    const int per_plane = (int)(((unsigned)rows + kRows - 1) / kRows), all = per_plane * (PLANES ? p.planes : 1), share = uniform((all + S - 1) / S);
     const int s0 = (int)blockIdx.y * share, count = all - s0 < share ? (all - s0 < 0 ? 0 : all - s0) : share;
 
     // where stage s lies: its plane, its first row of the group, how many are left of 64 (none past the last stage)
@@ -157,8 +164,11 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void grad_tiles(WeightGradParams p,
     const auto stage_at = [&](int s) {
         Stage r;
         const int at = s0 + s;
-        r.plane = (at >= 2 * per_plane ? 2 : at >= per_plane ? 1 : 0);
-        r.plane = r.plane < p.planes ? r.plane : p.planes - 1;
+        r.plane = 0;
+        if (PLANES) {
+            r.plane = at >= 2 * per_plane ? 2 : at >= per_plane ? 1 : 0;
+            r.plane = r.plane < p.planes ? r.plane : p.planes - 1;
+        }
         r.row = (at - r.plane * per_plane) * kRows;
         r.left = s < count ? (rows - r.row < kRows ? rows - r.row : kRows) : 0;
         return r;
@@ -205,7 +215,7 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void grad_tiles(WeightGradParams p,
     };
     const auto write_x = [&](int q, int h, const Stage &s, int buf) {
         i32x4 v = widened<CF>(codes[q][2 * h], codes[q][2 * h + 1], __uint_as_float((uint32_t)scale[q] << 23));
-        if (s.plane) v = finite_parts(v);
+        if (PLANES && s.plane) v = finite_parts(v);
         *reinterpret_cast<i32x4 *>(lds + buf * BUF + xto + q * XROWS * BK * 2 + h * 16) = v;
     };
 
@@ -232,13 +242,16 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void grad_tiles(WeightGradParams p,
             const Stage s = stage_at(b);
 #pragma unroll
             for (int q = 0; q < GL; ++q) load_g(q, s);
+            if (b < 2) {
 #pragma unroll
-            for (int q = 0; q < XL; ++q) load_x(q, s);
-            if (b == 2) break;  // (they stay in registers until buffer 0 is free)
+                for (int q = 0; q < XL; ++q) load_x(q, s);
 #pragma unroll
-            for (int q = 0; q < GL; ++q) write_g(q, b);
+                for (int q = 0; q < GL; ++q) write_g(q, b);
+            }
+            if (b == 0) {  // (what is not written stays in registers until its buffer is free)
 #pragma unroll
-            for (int q = 0; q < XL; ++q) write_x(q, 0, s, b), write_x(q, 1, s, b);
+                for (int q = 0; q < XL; ++q) write_x(q, 0, s, b), write_x(q, 1, s, b);
+            }
         }
         __syncthreads();
 #pragma unroll
@@ -246,11 +259,11 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void grad_tiles(WeightGradParams p,
 #pragma unroll
         for (int j = 0; j < FK; ++j) X[0][j] = read_x(j, 0, 0);
     }
-    const auto half = [&](auto which, int buf, int next, const Stage &s2, const Stage &s3) {
+    const auto half = [&](auto which, int buf, const Stage &s1, const Stage &s2, const Stage &s3) {
         constexpr int h = decltype(which)::value, o = h ^ 1;
-        // what goes between the instructions: reads, and in the second half writes and loads
-        constexpr int WORK = h ? 2 * GL + 3 * XL : 0, AHEAD = F / 2;
-        const int from = h ? next : buf;
+        // what goes between the instructions: reads, and writes and loads of one of the operands
+        constexpr int WORK = h ? 2 * GL : 3 * XL, AHEAD = F / 2;
+        const int from = h ? buf ^ 1 : buf;
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int t = 0; t < F; ++t) {
@@ -262,14 +275,14 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void grad_tiles(WeightGradParams p,
             if (j == FK - 1) G[i] = read_g(i, o, from);
 #pragma unroll
             for (int u = t * WORK / F; u < (t + 1) * WORK / F; ++u) {
-                if (u < GL)
-                    write_g(u, buf);
-                else if (u < GL + 2 * XL)
-                    write_x((u - GL) / 2, (u - GL) % 2, s2, buf);
-                else if (u < 2 * GL + 2 * XL)
-                    load_g(u - GL - 2 * XL, s3);
+                if (h && u % 2)
+                    load_g(u / 2, s3);
+                else if (h)
+                    write_g(u / 2, buf);
+                else if (u % 3 == 2)
+                    load_x(u / 3, s2);
                 else
-                    load_x(u - 2 * GL - 2 * XL, s3);
+                    write_x(u / 3, u % 3, s1, buf ^ 1);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -277,11 +290,11 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void grad_tiles(WeightGradParams p,
     typedef std::integral_constant<int, 0> First;
     typedef std::integral_constant<int, 1> Second;
     for (int s = 0, buf = 0; s < count; ++s, buf ^= 1) {
-        const Stage s2 = stage_at(s + 2), s3 = stage_at(s + 3);
-        half(First{}, buf, buf ^ 1, s2, s3);
+        const Stage s1 = stage_at(s + 1), s2 = stage_at(s + 2), s3 = stage_at(s + 3);
+        half(First{}, buf, s1, s2, s3);
         __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave has read buffer s and written its part of s + 1
         __builtin_amdgcn_s_barrier();
-        half(Second{}, buf, buf ^ 1, s2, s3);
+        half(Second{}, buf, s1, s2, s3);
     }
     const int64_t n = n0 + wn + (lane & 15);
     const bool whole = cols_n == BN && cols_k == BK;
@@ -364,15 +377,15 @@ GradPlan make_plan(int64_t T, int E, int64_t N, int64_t K, int g_dtype, bool g_a
     return p;
 }
 
-template <int CF>
+template <int CF, bool PLANES>
 void launch_tiles(const WeightGradParams &p, const GradPlan &plan, float *part, hipStream_t stream)
 {
     const int64_t side = plan.large ? 256 : 128, tn = ceil_div(p.N, side), tk = ceil_div(p.K, side);
     const dim3 grid((unsigned)(tn * tk * (p.E ? p.E : 1)), (unsigned)plan.S);
     if (plan.large)
-        hipLaunchKernelGGL((grad_tiles<CF, 256, 256, 2, 4>), grid, dim3(512), 0, stream, p, (int)tn, (int)tk, plan.S, part);
+        hipLaunchKernelGGL((grad_tiles<CF, PLANES, 256, 256, 2, 4>), grid, dim3(512), 0, stream, p, (int)tn, (int)tk, plan.S, part);
     else
-        hipLaunchKernelGGL((grad_tiles<CF, 128, 128, 2, 2>), grid, dim3(256), 0, stream, p, (int)tn, (int)tk, plan.S, part);
+        hipLaunchKernelGGL((grad_tiles<CF, PLANES, 128, 128, 2, 2>), grid, dim3(256), 0, stream, p, (int)tn, (int)tk, plan.S, part);
 }
 
 template <typename G, int PLANES>
@@ -423,10 +436,9 @@ hipError_t launch_weight_grad(int g_dtype, int c_dtype, const WeightGradParams &
     }
     at += plan.c_bytes;
     float *part = plan.S > 1 ? reinterpret_cast<float *>(at) : nullptr;
-    if (c_dtype == EMU_DT_E4M3FN)
-        launch_tiles<0>(p, plan, part, stream);
-    else
-        launch_tiles<1>(p, plan, part, stream);
+    const bool e4 = c_dtype == EMU_DT_E4M3FN, planes = plan.planes > 1;
+    (e4 ? planes ? launch_tiles<0, true> : launch_tiles<0, false> : planes ? launch_tiles<1, true> : launch_tiles<1, false>)(
+        p, plan, part, stream);
     if (part)
         hipLaunchKernelGGL(grad_join, dim3((unsigned)ceil_div((p.E ? p.E : 1) * p.N * ceil_div(p.K, 4), 256)), dim3(256), 0, stream, p,
                            part, plan.S);
