@@ -20,7 +20,7 @@ constexpr float kLargest = Q == EMU_DT_E4M3FN ? 448.0f : 57344.0f;
 // A block's scale and what makes codes of it.
 struct BlockScale {
     float value;      // the scale
-    float hi, lo;     // its reciprocal: exact in hi (e8m0), or the sum of both
+    float hi, lo;     // its reciprocal: exact in hi (e8m0), or the sum of both to within 2^-44
     uint32_t byte;    // e8m0
 };
 
@@ -44,9 +44,8 @@ __device__ __forceinline__ BlockScale scale_of(float most)
     } else {
         const float v = most / kLargest<Q>;
         s.value = finite ? (v > kLeastScale ? v : kLeastScale) : NAN;
-        const double r = 1.0 / (double)s.value;
-        s.hi = (float)r;
-        s.lo = (float)(r - (double)s.hi);
+        s.hi = __builtin_amdgcn_rcpf(s.value);
+        s.lo = __builtin_fmaf(-s.value, s.hi, 1.0f) * s.hi;
         s.byte = 0;
     }
     return s;
@@ -75,10 +74,10 @@ __device__ __forceinline__ uint32_t from_border(float y)
     return normal ? (bits & (2 * half - 1)) ^ half : size ? bits & (half - 1) : 1;
 }
 
-// 8 codes of v.  Binary32 scales: the quotient is rounded once, by the
-// reciprocal's two parts, and falls on the wrong side of a border between two
-// codes only if it lies on one; where any does, all are divided.  Values past the type's largest (by the scale's own rounding)
-// become it.
+// 8 codes of v.  Binary32 scales: v times the reciprocal's two parts is the
+// quotient to within 2^-30 before it is rounded, so it may fall on a border
+// between two codes, but never past one; where any does, all are divided.
+// Values past the type's largest (by the scale's own rounding) become it.
 template <int Q, bool E8M0>
 __device__ __forceinline__ uint2 codes_of(const f32x8 &v, const BlockScale &s)
 {
@@ -280,22 +279,30 @@ __global__ __launch_bounds__(256) void quant_squares(BlockQuantParams p)
 
 // ---- the gated activation ------------------------------------------------
 
-// p = 1 / (1 + exp(-a)) and q = 1 - p.  exp(-a) is 2^t with what t's rounding
-// cut off put back; where it overflows p is 0.
-struct Sigmoid {
-    float p, q;
-};
-__device__ __forceinline__ Sigmoid sigmoid(float a)
+// p = 1 / (1 + exp(-a)) of 8 values, and exp(-a), which is 2^t with what t's
+// rounding cut off put back; where it overflows p is 0.  The reciprocal is the
+// hardware's with one step of Newton's, within a unit of the last place, unless
+// a value is so far out that p is all but subnormal.
+__device__ __forceinline__ f32x8 sigmoid(const f32x8 &a, f32x8 &e)
 {
     constexpr float log2e = 1.44269502f, rest = 1.92596299e-8f, ln2 = 0.693147181f;
-    const float t = -a * log2e;
-    const float cut = __builtin_fmaf(-a, log2e, -t) - a * rest;
-    float e = __builtin_amdgcn_exp2f(t);
-    e = __builtin_fabsf(t) < 126.0f ? __builtin_fmaf(e, cut * ln2, e) : e;
-    Sigmoid s;
-    s.p = 1.0f / (1.0f + e);
-    s.q = e > 1.0f ? 1.0f - s.p : e * s.p;  // (no infinity meets a zero)
-    return s;
+    float most = 0.0f;
+    f32x8 p;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float t = -a[i] * log2e;
+        const float cut = __builtin_fmaf(-a[i], log2e, -t) - a[i] * rest;
+        const float x = __builtin_amdgcn_exp2f(t);
+        e[i] = __builtin_fabsf(t) < 126.0f ? __builtin_fmaf(x, cut * ln2, x) : x;
+        most = __builtin_elementwise_maximum(most, e[i]);
+        const float d = 1.0f + e[i], near = __builtin_amdgcn_rcpf(d);
+        p[i] = __builtin_fmaf(__builtin_fmaf(-d, near, 1.0f), near, near);
+    }
+    if (__any(!(most < 1.2676506e30f))) {  // 2^100, or a NaN
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = 1.0f / (1.0f + e[i]);
+    }
+    return p;
 }
 
 // KEEP: gate's and up's own codes are stored too.
@@ -318,9 +325,8 @@ __global__ __launch_bounds__(256) void swiglu_rows(SwigluParams p, int per_row)
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
         const f32x8 g = settle8<X>(raw[i][0], at[i].c, n), u = settle8<X>(raw[i][1], at[i].c, n);
-        f32x8 h;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) h[j] = g[j] * sigmoid(g[j]).p * u[j];
+        f32x8 e;
+        const f32x8 h = g * sigmoid(g, e) * u;
         const BlockScale s = scale_of<Q, E8M0>(most_of_16(most_of(h)));
         BlockScale sg, su;
         if (KEEP) {
@@ -371,12 +377,13 @@ __global__ __launch_bounds__(256) void swiglu_grad_rows(SwigluGradParams p, int 
         if (!at[i].in) continue;
         const f32x8 g = settle8<G>(raw[i], at[i].c, n), a = values_of<Q>(codes[i][0]) * s[i][0],
                     b = values_of<Q>(codes[i][1]) * s[i][1];
-        f32x8 da, db;
+        f32x8 da, db, e;
+        const f32x8 s = sigmoid(a, e);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const Sigmoid t = sigmoid(a[j]);
-            da[j] = g[j] * b[j] * (t.p * __builtin_fmaf(a[j], t.q, 1.0f));
-            db[j] = g[j] * (a[j] * t.p);
+            const float rest = e[j] > 1.0f ? 1.0f - s[j] : e[j] * s[j];  // (no infinity meets a zero)
+            da[j] = g[j] * b[j] * (s[j] * __builtin_fmaf(a[j], rest, 1.0f));
+            db[j] = g[j] * (a[j] * s[j]);
         }
         G *out = static_cast<G *>(p.grad) + at[i].row * p.ldgrad;
         with_bool(p.once, [&](auto once) {
