@@ -30,9 +30,9 @@ template <typename G, int PLANES>
 __global__ __launch_bounds__(256) void split_planes(const G *g, int64_t ldg, int64_t T, int64_t N, uint16_t *out, int64_t ldo,
                                                     int64_t plane)
 {
-    const int64_t chunks = ldo / 8, id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t t = id / chunks;
-    const int c = (int)(id % chunks) * 8, n = (int)N;
+    const uint32_t chunks = (uint32_t)(ldo / 8), id = blockIdx.x * 256 + threadIdx.x, row = id / chunks;
+    const int64_t t = row;
+    const int c = (int)(id - row * chunks) * 8, n = (int)N;
     if (t >= T) return;
     f32x8 v = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
     if (c < n) v = settle8<G>(fetch8(g + t * ldg, c, n), c, n);
@@ -60,10 +60,10 @@ __global__ __launch_bounds__(256) void split_planes(const G *g, int64_t ldg, int
 // lane gets consecutive rows of its column.  While a half is multiplied out of
 // registers the next is read:
 //   (s, 0): multiply; read the fragments of (s, 1), write the codes of s + 1 into
-//           the other buffer and load those of s + 2;
+//           the other buffer and load those of s + 2 (or of s + 3, AHEAD 2);
 //   wait until every wave has written s + 1 and read buffer s (one barrier a stage);
 //   (s, 1): multiply; read the fragments of (s + 1, 0), write g of s + 2 into buffer
-//           s and load that of s + 3.
+//           s and load that of s + 3 (s + 4).
 // LDS bounds it: a stage of 64 rows writes 64 KiB and reads 192 to 2048 cycles of
 // products, and 16384 x 8192 x 4096 in 8 groups (920 us) takes 750 without the
 // writes and 820 without the reads.  With both operands' writes in one half, 936.
@@ -114,10 +114,13 @@ __device__ __forceinline__ s16x4 read_turned(const int8_t *lds)
 }
 
 // part: null, or [S, E, N, K] sums of each split of a group's rows (grid y).
+// AHEAD: the stages between the last one written and the last one loaded, in as
+// many sets of registers (one of 256 x 256 has none to spare; 128 x 128: two take
+// 18.9 us for 1024 x 1920 x 1920, one 20).
 // PLANES: g may have more planes than one (without the test in the writes, one
 // plane of 16384 x 8192 x 4096 in 8 groups takes 945 us for 976, 1024 x 1920 x
 // 1920 21.0 for 23.0).
-template <int CF, bool PLANES, int BN, int BK, int WN, int WK>
+template <int CF, bool PLANES, int BN, int BK, int WN, int WK, int AHEAD>
 __global__ __launch_bounds__(WN *WK * 64, 2) void grad_tiles(WeightGradParams p, int tn, int tk, int S,
                                                                                                 float *part)
 {
@@ -190,13 +193,13 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void grad_tiles(WeightGradParams p,
 #pragma unroll
     for (int q = 0; q < GL; ++q)
         gfrom[variant(q)] = lane / GC * ldg2 + ((lane % GC) ^ (turn(grow + GROWS * q + lane / GC) * 2)) * 16;
-    i32x4 graw[GL];
-    const auto load_g = [&](int q, const Stage &s) {
-        graw[q] = load_within(p.g + s.plane * p.plane_stride + (int64_t)(first + s.row) * p.ldg + n0, range(s.left, ldg2, cols_n * 2),
+    i32x4 graw[AHEAD][GL];
+    const auto load_g = [&](int set, int q, const Stage &s) {
+        graw[set][q] = load_within(p.g + s.plane * p.plane_stride + (int64_t)(first + s.row) * p.ldg + n0, range(s.left, ldg2, cols_n * 2),
                               gfrom[variant(q)] + (grow + q * GROWS) * ldg2);
     };
-    const auto write_g = [&](int q, int buf) {
-        *reinterpret_cast<i32x4 *>(lds + buf * BUF + (wave * GL + q) * 1024 + lane * 16) = graw[q];
+    const auto write_g = [&](int set, int q, int buf) {
+        *reinterpret_cast<i32x4 *>(lds + buf * BUF + (wave * GL + q) * 1024 + lane * 16) = graw[set][q];
     };
     // codes: 16 a lane, XROWS rows with each of a workgroup's loads
     constexpr int XROWS = threads / XC;
@@ -205,16 +208,16 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void grad_tiles(WeightGradParams p,
     const int xfrom = xrow * ldc + xchunk * 16, xto = GBUF + xrow * BK * 2 + (xchunk ^ turn(xrow)) * 32;
     const int last_block = (int)(blocks_of(p.K) - 1 - k0 / kBlock), xblock = xchunk * 16 / kBlock;
     const uint8_t *const xscale = p.scales + (k0 / kBlock + (xblock < last_block ? xblock : last_block)) * p.s_block;
-    i32x4 codes[XL];
-    int scale[XL];
-    const auto load_x = [&](int q, const Stage &s) {
-        codes[q] = load_within(p.codes + (int64_t)(first + s.row) * p.ldc + k0, range(s.left, ldc, cols_k), xfrom + q * XROWS * ldc);
+    i32x4 codes[AHEAD][XL];
+    int scale[AHEAD][XL];
+    const auto load_x = [&](int set, int q, const Stage &s) {
+        codes[set][q] = load_within(p.codes + (int64_t)(first + s.row) * p.ldc + k0, range(s.left, ldc, cols_k), xfrom + q * XROWS * ldc);
         // (rows past the group's last have the last one's: their codes are zeros, and a NaN is in its block anyway)
         const int t = s.row + xrow + q * XROWS;
-        scale[q] = xscale[(int64_t)(first + (t < rows ? t : rows - 1)) * p.s_row];
+        scale[set][q] = xscale[(int64_t)(first + (t < rows ? t : rows - 1)) * p.s_row];
     };
-    const auto write_x = [&](int q, int h, const Stage &s, int buf) {
-        i32x4 v = widened<CF>(codes[q][2 * h], codes[q][2 * h + 1], __uint_as_float((uint32_t)scale[q] << 23));
+    const auto write_x = [&](int set, int q, int h, const Stage &s, int buf) {
+        i32x4 v = widened<CF>(codes[set][q][2 * h], codes[set][q][2 * h + 1], __uint_as_float((uint32_t)scale[set][q] << 23));
         if (PLANES && s.plane) v = finite_parts(v);
         *reinterpret_cast<i32x4 *>(lds + buf * BUF + xto + q * XROWS * BK * 2 + h * 16) = v;
     };
@@ -238,20 +241,25 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void grad_tiles(WeightGradParams p,
     bf16x8 G[FN], X[2][FK];
     if (count) {
 #pragma unroll
-        for (int b = 0; b < 3; ++b) {
+        for (int b = 0; b < AHEAD + 2; ++b) {
+            // (what is not written stays in registers until its buffer is free)
+            if (b == AHEAD) {
+                const Stage s = stage_at(0);
+#pragma unroll
+                for (int q = 0; q < GL; ++q) write_g(0, q, 0);
+#pragma unroll
+                for (int q = 0; q < XL; ++q) write_x(0, q, 0, s, 0), write_x(0, q, 1, s, 0);
+            }
+            if (b == AHEAD + 1) {
+#pragma unroll
+                for (int q = 0; q < GL; ++q) write_g(1 % AHEAD, q, 1);
+            }
             const Stage s = stage_at(b);
 #pragma unroll
-            for (int q = 0; q < GL; ++q) load_g(q, s);
-            if (b < 2) {
+            for (int q = 0; q < GL; ++q) load_g(b % AHEAD, q, s);
+            if (b == AHEAD + 1) break;
 #pragma unroll
-                for (int q = 0; q < XL; ++q) load_x(q, s);
-#pragma unroll
-                for (int q = 0; q < GL; ++q) write_g(q, b);
-            }
-            if (b == 0) {  // (what is not written stays in registers until its buffer is free)
-#pragma unroll
-                for (int q = 0; q < XL; ++q) write_x(q, 0, s, b), write_x(q, 1, s, b);
-            }
+            for (int q = 0; q < XL; ++q) load_x(b % AHEAD, q, s);
         }
         __syncthreads();
 #pragma unroll
@@ -259,42 +267,49 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void grad_tiles(WeightGradParams p,
 #pragma unroll
         for (int j = 0; j < FK; ++j) X[0][j] = read_x(j, 0, 0);
     }
-    const auto half = [&](auto which, int buf, const Stage &s1, const Stage &s2, const Stage &s3) {
-        constexpr int h = decltype(which)::value, o = h ^ 1;
+    const auto half = [&](auto which, auto parity, const Stage &now, const Stage &then, int buf) {
+        constexpr int h = decltype(which)::value, o = h ^ 1, set = (h + decltype(parity)::value + 1) % AHEAD;
         // what goes between the instructions: reads, and writes and loads of one of the operands
-        constexpr int WORK = h ? 2 * GL : 3 * XL, AHEAD = F / 2;
+        constexpr int WORK = h ? 2 * GL : 3 * XL;
         const int from = h ? buf ^ 1 : buf;
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int t = 0; t < F; ++t) {
             const int i = t / FK, j = t % FK;
 #pragma unroll
-            for (int u = t * FK / AHEAD; u < FK && u < (t + 1) * FK / AHEAD; ++u) X[o][u] = read_x(u, o, from);
+            for (int u = t * FK / (F / 2); u < FK && u < (t + 1) * FK / (F / 2); ++u) X[o][u] = read_x(u, o, from);
             acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(X[h][j], G[i], acc[i][j], 0, 0, 0);
             __builtin_amdgcn_sched_barrier(0);
             if (j == FK - 1) G[i] = read_g(i, o, from);
 #pragma unroll
             for (int u = t * WORK / F; u < (t + 1) * WORK / F; ++u) {
                 if (h && u % 2)
-                    load_g(u / 2, s3);
+                    load_g(set, u / 2, then);
                 else if (h)
-                    write_g(u / 2, buf);
+                    write_g(set, u / 2, buf);
                 else if (u % 3 == 2)
-                    load_x(u / 3, s2);
+                    load_x(set, u / 3, then);
                 else
-                    write_x(u / 3, u % 3, s1, buf ^ 1);
+                    write_x(set, u / 3, u % 3, now, buf ^ 1);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
     };
     typedef std::integral_constant<int, 0> First;
     typedef std::integral_constant<int, 1> Second;
-    for (int s = 0, buf = 0; s < count; ++s, buf ^= 1) {
-        const Stage s1 = stage_at(s + 1), s2 = stage_at(s + 2), s3 = stage_at(s + 3);
-        half(First{}, buf, s1, s2, s3);
+    const auto stage = [&](auto parity, int s, int buf) {
+        const Stage next = stage_at(s + 1), x = stage_at(s + 1 + AHEAD), g = stage_at(s + 2 + AHEAD);
+        half(First{}, parity, next, x, buf);
         __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave has read buffer s and written its part of s + 1
         __builtin_amdgcn_s_barrier();
-        half(Second{}, buf, s1, s2, s3);
+        half(Second{}, parity, next, g, buf);
+    };
+    if constexpr (AHEAD == 1) {
+        for (int s = 0, buf = 0; s < count; ++s, buf ^= 1) stage(First{}, s, buf);
+    } else {
+        int s = 0;
+        for (; s + 1 < count; s += 2) stage(First{}, s, 0), stage(Second{}, s + 1, 1);
+        if (s < count) stage(First{}, s, 0);
     }
     const int64_t n = n0 + wn + (lane & 15);
     const bool whole = cols_n == BN && cols_k == BK;
@@ -353,9 +368,10 @@ GradPlan make_plan(int64_t T, int E, int64_t N, int64_t K, int g_dtype, bool g_a
     p.ldc = blocks_of(K) * kBlock;
     p.g_bytes = p.split_g ? (p.planes * T * p.ldg * 2 + 15) / 16 * 16 : 0;
     p.c_bytes = p.repack_c ? T * p.ldc : 0;
-    // The fastest estimate, as for the products: a round of 256 tiles (512
-    // small ones, two to a CU) takes its stages' time, a split of rows 5 us
-    // more and its sums at 4 TB/s, there and back.
+    // The fastest estimate, as for the products: a round of 256 large tiles, or of
+    // 512 small ones, two to a CU, or a rest of up to 256, one to a CU, as measured
+    // (4096 x 4096 of 1024 rows: 43 us large, 51 small; 2048 x 2048: 35 and 20); a
+    // split of rows 5 us more and its sums at 4 TB/s, there and back.
     const int64_t stages = ceil_div(ceil_div(T, groups), kRows) * p.planes;
     double best = 0.0;
     p.S = 1;
@@ -365,7 +381,10 @@ GradPlan make_plan(int64_t T, int E, int64_t N, int64_t K, int g_dtype, bool g_a
             if (S > 1 && stages / S < 4) break;
             const int64_t side = large ? 256 : 128;
             const int64_t tiles = ceil_div(N, side) * ceil_div(K, side) * groups * S;
-            double us = (double)ceil_div(tiles, large ? 256 : 512) * (2.0 + (double)ceil_div(stages, S) * (large ? 1.3 : 0.8));
+            const int64_t rest = large ? 0 : tiles % 512 <= 256 ? tiles % 512 : 0;
+            const double each = (double)ceil_div(stages, S);
+            double us = (double)ceil_div(tiles - rest, large ? 256 : 512) * (large ? 6.0 + each * 1.65 : 5.0 + each * 1.2);
+            if (rest) us += 4.0 + each * 0.7;
             if (S > 1) us += 5.0 + (double)S * (double)groups * (double)N * (double)K * 8.0 / 4e6;
             if (any && us >= best) continue;
             any = true;
@@ -383,9 +402,9 @@ void launch_tiles(const WeightGradParams &p, const GradPlan &plan, float *part, 
     const int64_t side = plan.large ? 256 : 128, tn = ceil_div(p.N, side), tk = ceil_div(p.K, side);
     const dim3 grid((unsigned)(tn * tk * (p.E ? p.E : 1)), (unsigned)plan.S);
     if (plan.large)
-        hipLaunchKernelGGL((grad_tiles<CF, PLANES, 256, 256, 2, 4>), grid, dim3(512), 0, stream, p, (int)tn, (int)tk, plan.S, part);
+        hipLaunchKernelGGL((grad_tiles<CF, PLANES, 256, 256, 2, 4, 1>), grid, dim3(512), 0, stream, p, (int)tn, (int)tk, plan.S, part);
     else
-        hipLaunchKernelGGL((grad_tiles<CF, PLANES, 128, 128, 2, 2>), grid, dim3(256), 0, stream, p, (int)tn, (int)tk, plan.S, part);
+        hipLaunchKernelGGL((grad_tiles<CF, PLANES, 128, 128, 2, 2, 2>), grid, dim3(256), 0, stream, p, (int)tn, (int)tk, plan.S, part);
 }
 
 template <typename G, int PLANES>
