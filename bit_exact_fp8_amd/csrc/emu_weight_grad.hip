@@ -70,11 +70,14 @@ __global__ __launch_bounds__(256) void split_planes(const G *g, int64_t ldg, int
 // (Loads straight into LDS would spare g its way through registers, but the
 // compiler then waits for all of them before each read that turns: 2.4 ms for 1.2.)
 // 16 rows' segments of 32 bytes meet in one read: row t's pair of chunks of 16
-// bytes c stands at place c ^ ((t & 3) + 4 (t / 8 & 1)), which spreads them over all banks.
+// bytes c stands at place c ^ ((t & 3) + 4 (t / 8 & 1)), which spreads them over all
+// banks.  Of codes' pairs those of every other four stand with their second chunk
+// first, so that 8 lanes that write a chunk of each meet all banks too (944 us, 935).
 
 constexpr int kRows = 64;
 
 __device__ __forceinline__ int turn(int t) { return (t & 3) | (t >> 1 & 4); }
+__device__ __forceinline__ int half_of(int c) { return (c & 4) << 2; }
 
 template <int BN, int BK>
 constexpr int kGradLds = 2 * kRows * (BN + BK) * 2;
@@ -205,7 +208,7 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void grad_tiles(WeightGradParams p,
     constexpr int XROWS = threads / XC;
     static_assert(XROWS % 16 == 0 && (VARIANTS < 4 || GL <= 8), "a lane's places turn alike in all of its loads");
     const int xrow = (int)threadIdx.x / XC, xchunk = (int)threadIdx.x % XC, ldc = (int)p.ldc;
-    const int xfrom = xrow * ldc + xchunk * 16, xto = GBUF + xrow * BK * 2 + (xchunk ^ turn(xrow)) * 32;
+    const int xfrom = xrow * ldc + xchunk * 16, xto = GBUF + xrow * BK * 2 + (xchunk ^ turn(xrow)) * 32 + half_of(xchunk);
     const int last_block = (int)(blocks_of(p.K) - 1 - k0 / kBlock), xblock = xchunk * 16 / kBlock;
     const uint8_t *const xscale = p.scales + (k0 / kBlock + (xblock < last_block ? xblock : last_block)) * p.s_block;
     i32x4 codes[AHEAD][XL];
@@ -219,7 +222,7 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void grad_tiles(WeightGradParams p,
     const auto write_x = [&](int set, int q, int h, const Stage &s, int buf) {
         i32x4 v = widened<CF>(codes[set][q][2 * h], codes[set][q][2 * h + 1], __uint_as_float((uint32_t)scale[set][q] << 23));
         if (PLANES && s.plane) v = finite_parts(v);
-        *reinterpret_cast<i32x4 *>(lds + buf * BUF + xto + q * XROWS * BK * 2 + h * 16) = v;
+        *reinterpret_cast<i32x4 *>(lds + buf * BUF + (h ? xto ^ 16 : xto) + q * XROWS * BK * 2) = v;
     };
 
     // fragments: this lane's place in rows 8 (lane / 16) + (lane / 4 & 3) of a half, and 4 below
@@ -229,7 +232,7 @@ __global__ __launch_bounds__(WN *WK * 64, 2) void grad_tiles(WeightGradParams p,
 #pragma unroll
     for (int i = 0; i < FN; ++i) gat[i] = trow * BN * 2 + (((wn / 16 + i) ^ turn(trow)) * 32) + (lane & 3) * 8;
 #pragma unroll
-    for (int j = 0; j < FK; ++j) xat[j] = GBUF + trow * BK * 2 + (((wk / 16 + j) ^ turn(trow)) * 32) + (lane & 3) * 8;
+    for (int j = 0; j < FK; ++j) xat[j] = GBUF + trow * BK * 2 + (((wk / 16 + j) ^ turn(trow)) * 32) + ((lane & 3) * 8 ^ half_of(wk / 16 + j));
     const auto turned = [&](int at, int row_bytes) {
         const s16x4 a = read_turned(lds + at), b = read_turned(lds + at + 4 * row_bytes);
         return __builtin_bit_cast(bf16x8, s16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]});
