@@ -67,8 +67,8 @@ struct Tile {
     int bm, bn, per_cu;
     double ends, stage, stage2;
 };
-constexpr Tile kTiles[] = {{64, 64, 2, 3.0, 0.28, 0.45}, {128, 128, 2, 4.0, 0.84, 1.25}, {256, 128, 1, 6.0, 1.02, 0}, {256, 256, 1, 12.0, 1.45, 0}};
-constexpr double kStageOf[] = {1.0, 1.1, 2.0};  // of each mode, relative to kHardware
+constexpr Tile kTiles[] = {{64, 64, 2, 3.0, 0.28, 0.45}, {128, 128, 2, 4.0, 0.80, 1.15}, {256, 128, 1, 6.0, 0.92, 0}, {256, 256, 1, 12.0, 1.45, 0}};
+constexpr double kStageOf[] = {1.0, 1.2, 2.0};  // of each mode, relative to kHardware
 
 double tiles_us(const Tile &t, int64_t tiles, int64_t stages, int mode)
 {

@@ -1,8 +1,8 @@
 // ops_binding.cpp -- the Python side of include/emu_operators.h and
 // emu_block_operators.h for torch tensors: argument checks, outputs, workspaces
-// and the call on torch's current stream.  Compiled, since a decoded token's call is shorter on the
-// GPU than its checks are in Python (1 x 5760 x 1920 int8: 10.5 us a call with
-// a binding through ctypes, the kernel 5).
+// and the call on torch's current stream.  Compiled, since a decoded token's
+// call is shorter on the GPU than its checks are in Python (1 x 5760 x 1920 int8:
+// 10.5 us a call with a binding through ctypes, the kernel 5).
 //
 // The emu_* functions are those of the library that is loaded before this
 // module is (operators._binding).  Nothing is thrown across the C API: every
