@@ -615,6 +615,8 @@ void launch_mode(const BlockMMParams &p, const BlockPlan &plan, float *part, hip
         if (plan.tile == 1)
             launch_tiles<AF, WF, MODE, 128, 128, 2, 2, 2>(p, plan, part, stream);
         else if (plan.tile == 2)
+            launch_tiles<AF, WF, MODE, 64, 128, 2, 2, 3>(p, plan, part, stream);
+        else if (plan.tile == 3)
             launch_tiles<AF, WF, MODE, 256, 128, 4, 2, 3>(p, plan, part, stream);
         else
             launch_tiles<AF, WF, MODE, 256, 256, 2, 4, 2>(p, plan, part, stream);

@@ -67,7 +67,8 @@ struct Tile {
     int bm, bn, per_cu;
     double ends, stage, stage2;
 };
-constexpr Tile kTiles[] = {{64, 64, 2, 3.0, 0.28, 0.45}, {128, 128, 2, 4.0, 0.80, 1.15}, {256, 128, 1, 6.0, 0.92, 0}, {256, 256, 1, 12.0, 1.45, 0}};
+constexpr Tile kTiles[] = {{64, 64, 2, 3.0, 0.28, 0.45}, {128, 128, 2, 4.0, 0.80, 1.15}, {64, 128, 2, 3.5, 0.42, 0.70},
+                           {256, 128, 1, 6.0, 0.92, 0}, {256, 256, 1, 12.0, 1.45, 0}};
 constexpr double kStageOf[] = {1.0, 1.2, 2.0};  // of each mode, relative to kHardware
 
 double tiles_us(const Tile &t, int64_t tiles, int64_t stages, int mode)
@@ -114,7 +115,7 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int E, bool grouped, int mode, b
     // The fastest estimate; a split of K takes 5 us more and its sums at 4 TB/s,
     // there and back.  Each group's last tile is half full in the mean.
     double best = 0.0;
-    for (int i = 0; i < (mode == kExact ? 2 : 4); ++i)
+    for (int i = 0; i < (mode == kExact ? 2 : 5); ++i)
         for (int S = 1; S <= (grouped ? 1 : 8); S *= 2) {
             const int64_t stages = ceil_div(total, S);
             if (S > 1 && stages < 4) break;
@@ -129,7 +130,7 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int E, bool grouped, int mode, b
     // Up to 16 rows read w once, straight into registers, and wait for nothing,
     // but read a again for every 16 columns (16 x 4096 x 4096: 10.0 us, in tiles
     // 11.2; 16 x 8192 x 8192: 24.2 and 16.7).  Groups take tiles in any case: 32 x
-    // 4096 x 2048 over 16 of them 29.9 us, in tiles 26.4.
+    // 4096 x 2048 over 16 of them 29.9 us, in tiles 24.2.
     if (!grouped && M <= 16 && 2.5 + (double)N * (double)K * (1.0 + (double)M / 16.0) / 7.5e6 < best) {
         k.tile = -1;
         k.S = k.rows = 1;
