@@ -144,7 +144,8 @@ def block_weight_grad(grad: torch.Tensor, codes: torch.Tensor, scale: torch.Tens
     blocks of K] as ``block_quant`` gives them, scales float8_e8m0fnu (powers of
     two, under which bf16 holds x exactly).  ends [E]: a sum for each group of
     rows, [E, N, K], as in ``grouped_block_scaled_mm``; rows behind the last
-    group's take no part, and an empty group's sum is 0.  Products are exact and
-    added in float32; out_dtype is grad's where none is given.  grad in float16
-    or float32 takes two or three times as long as in bfloat16."""
+    group's take no part, and an empty group's sum is 0.  Products are exact (of
+    a float32 grad within 2^-17 where out_dtype has 16 bits) and added in
+    float32; out_dtype is grad's where none is given.  grad in float16 or float32
+    takes two or three times as long as in bfloat16."""
     return (_OPS or _binding()).block_weight_grad(grad, codes, scale, ends, out_dtype, out)

@@ -6,7 +6,9 @@
 // with scales that are powers of two bf16 holds code times scale exactly, and
 // v_mfma_f32_16x16x32_bf16 adds in binary32 (1.95 PFLOP/s of instructions alone).  g
 // in fp16 or fp32 is split into the two or three bf16 numbers whose sum it is, and
-// the product of each is added.
+// the product of each is added.  For outputs of 16 bits two stand for an fp32 g
+// too: what they leave of it, at most 2^-17, is little beside the output's rounding
+// (2^-9 or 2^-12), and the third costs as much as each of them.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -25,7 +27,9 @@ typedef short s16x8 __attribute__((ext_vector_type(8)));
 // ---- g in planes of bf16 -------------------------------------------------
 
 // Eight values a thread, cut to 8 significant bits, then what that left, and
-// what that left: each cut is exact, and no part is larger than the value.
+// what that left: each cut is exact, and no part is larger than the value.  Two
+// parts of an fp32 value are its nearest one (or cut, where that were an infinity)
+// and the nearest of what that left.
 template <typename G, int PLANES>
 __global__ __launch_bounds__(256) void split_planes(const G *g, int64_t ldg, int64_t T, int64_t N, uint16_t *out, int64_t ldo,
                                                     int64_t plane)
@@ -43,8 +47,13 @@ __global__ __launch_bounds__(256) void split_planes(const G *g, int64_t ldg, int
         for (int i = 0; i < 8; ++i) {
             const uint32_t bits = __float_as_uint(v[i]);
             const bool finite = (bits & 0x7F800000u) != 0x7F800000u, nan = v[i] != v[i];
-            r[i] = (uint16_t)(bits >> 16 | (nan ? 0x40u : 0u));
-            v[i] = finite ? v[i] - __uint_as_float(bits & 0xFFFF0000u) : 0.0f;
+            uint32_t part = bits >> 16 | (nan ? 0x40u : 0u);
+            if (sizeof(G) == 4 && PLANES == 2) {
+                const uint32_t near = (bits + 0x7FFFu + (bits >> 16 & 1u)) >> 16;
+                part = (near & 0x7F80u) != 0x7F80u ? near : part;
+            }
+            r[i] = (uint16_t)part;
+            v[i] = finite ? v[i] - __uint_as_float(part << 16) : 0.0f;
         }
         *reinterpret_cast<Raw8<uint16_t> *>(out + p * plane + t * ldo + c) = r;
     }
@@ -360,11 +369,11 @@ struct GradPlan {
     int64_t g_bytes, c_bytes, part_bytes;
 };
 
-GradPlan make_plan(int64_t T, int E, int64_t N, int64_t K, int g_dtype, bool g_aligned, bool c_aligned)
+GradPlan make_plan(int64_t T, int E, int64_t N, int64_t K, int g_dtype, bool out16, bool g_aligned, bool c_aligned)
 {
     GradPlan p{};
     const int64_t groups = E ? E : 1;
-    p.planes = g_dtype == EMU_DT_BF16 ? 1 : g_dtype == EMU_DT_FP16 ? 2 : 3;
+    p.planes = g_dtype == EMU_DT_BF16 ? 1 : g_dtype == EMU_DT_FP16 || out16 ? 2 : 3;
     p.split_g = p.planes > 1 || !g_aligned;
     p.repack_c = !c_aligned;
     p.ldg = ceil_div(N, 8) * 8;
@@ -426,15 +435,20 @@ void launch_split(const WeightGradParams &p, uint16_t *out, int64_t ldo, hipStre
 
 int64_t weight_grad_workspace(int64_t T, int E, int64_t N, int64_t K, int g_dtype, bool g_aligned, bool c_aligned)
 {
-    const GradPlan p = make_plan(T, E, N, K, g_dtype, g_aligned, c_aligned);
-    return p.g_bytes + p.c_bytes + p.part_bytes;
+    int64_t most = 0;  // of either kind of output
+    for (const bool out16 : {false, true}) {
+        const GradPlan p = make_plan(T, E, N, K, g_dtype, out16, g_aligned, c_aligned);
+        const int64_t bytes = p.g_bytes + p.c_bytes + p.part_bytes;
+        most = bytes > most ? bytes : most;
+    }
+    return most;
 }
 
 hipError_t launch_weight_grad(int g_dtype, int c_dtype, const WeightGradParams &params, bool g_aligned, bool c_aligned, void *ws,
                               hipStream_t stream)
 {
     WeightGradParams p = params;
-    const GradPlan plan = make_plan(p.T, p.E, p.N, p.K, g_dtype, g_aligned, c_aligned);
+    const GradPlan plan = make_plan(p.T, p.E, p.N, p.K, g_dtype, p.out_dtype != EMU_DT_FP32, g_aligned, c_aligned);
     char *at = static_cast<char *>(ws);
     p.planes = plan.planes;
     if (plan.split_g && p.T > 0) {
@@ -443,6 +457,8 @@ hipError_t launch_weight_grad(int g_dtype, int c_dtype, const WeightGradParams &
             launch_split<__bf16, 1>(p, g, plan.ldg, stream);
         else if (g_dtype == EMU_DT_FP16)
             launch_split<_Float16, 2>(p, g, plan.ldg, stream);
+        else if (plan.planes == 2)
+            launch_split<float, 2>(p, g, plan.ldg, stream);
         else
             launch_split<float, 3>(p, g, plan.ldg, stream);
         p.g = g;

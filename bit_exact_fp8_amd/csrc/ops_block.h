@@ -105,7 +105,7 @@ enum BlockMode {
 };
 struct BlockPlan {
     int mode;        // BlockMode
-    int tile;        // of kBlockTiles, or -1: few rows
+    int tile;        // of the plan's tiles, or -1: few rows
     int rows;        // few rows: fragments of 16 of them
     int waves;       // few rows: waves of a workgroup
     bool words;      // few rows: the operands' rows are aligned to 4 bytes

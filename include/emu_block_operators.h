@@ -146,7 +146,8 @@ EMU_API size_t emu_grouped_block_scaled_mm_workspace(int64_t T, int64_t E, int64
  * g [T, N] bf16, fp16 or fp32; codes [T, K] e4m3fn or e5m2, blocks of 1 x 128
  * with e8m0 scales, that of row t and block b at t s_row + b s_block; out of
  * any of g's types.  Products are exact (those of fp16 and fp32 g as two and
- * three parts) and added in binary32; an out of no rows is 0.
+ * three parts; for outputs of 16 bits those of fp32 g as two, within 2^-17) and
+ * added in binary32; an out of no rows is 0.
  * ends NULL: one sum over all rows, out [N, K].  Else E sums by groups of
  * rows, as in emu_grouped_block_scaled_mm: out [E, N, K], out_stride elements
  * between matrices, and rows behind the last group's take no part.
