@@ -701,6 +701,24 @@ def test_weight_grad_special_values(dev, g_t):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("g_t", [BF, HF, SF])
+@pytest.mark.parametrize("out", [BF, SF])
+def test_weight_grad_of_infinities(dev, g_t, out):
+    """An infinite code beside whole, short, infinite and vanishing gradients, each in a column of its own."""
+    g = torch.tensor([1.0, -3.0, 0.75, INF, -INF, 0.0, 2.0 ** -20, -1.0 - 2.0 ** -7, math.nan]).expand(3, 9).clone()
+    g[:2] = 1.0
+    c = torch.zeros(3, 128)
+    c[2] = 1.0
+    c[2, 5], c[2, 6], c[2, 7] = INF, -INF, 0.0
+    s = torch.ones(3, 1, device=dev).to(E8)
+    y = fw.block_weight_grad(g.to(g_t).to(dev), c.to(E5).to(dev), s, out_dtype=out).cpu().to(f64)
+    want = g.to(g_t).to(f64).t() @ c.to(f64)
+    finite = want.isfinite()
+    assert torch.equal(finite, y.isfinite()) and torch.equal(want[~finite].nan_to_num(nan=7.0), y[~finite].nan_to_num(nan=7.0))
+    close(y[finite], want[finite], half_step(want[finite], out) + F * want[finite].abs(), "weights' gradient")
+
+
+@pytest.mark.gpu
 def test_weight_grad_of_far_scales_and_axes(dev):
     """Scales over the whole of bf16's range; leading axes; no groups at all."""
     gen = rng(6)
