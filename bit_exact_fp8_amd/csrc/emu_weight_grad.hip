@@ -50,7 +50,7 @@ __global__ __launch_bounds__(256) void split_planes(const G *g, int64_t ldg, int
             uint32_t part = bits >> 16 | (nan ? 0x40u : 0u);
             if (sizeof(G) == 4 && PLANES == 2) {
                 const uint32_t near = (bits + 0x7FFFu + (bits >> 16 & 1u)) >> 16;
-                part = (near & 0x7F80u) != 0x7F80u ? near : part;
+                part = finite && (near & 0x7F80u) != 0x7F80u ? near : part;
             }
             r[i] = (uint16_t)part;
             v[i] = finite ? v[i] - __uint_as_float(part << 16) : 0.0f;

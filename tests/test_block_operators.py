@@ -719,6 +719,20 @@ def test_weight_grad_of_infinities(dev, g_t, out):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("out", [BF, HF, SF])
+def test_weight_grad_of_every_nan(dev, out):
+    """Each pattern of a binary32 NaN is one in each of its parts' products."""
+    patterns = [0x7F800001, 0x7FBFFFFF, 0x7FC00000, 0x7FFF7FFF, 0x7FFF8000, 0x7FFFFFFF]
+    g = torch.tensor(patterns + [p - 2 ** 31 for p in patterns] + [0x7F7FFFFF, 0x7F7F8000, -0x00800001, 1], dtype=torch.int32)[None]
+    c = torch.zeros(1, 128)
+    c[0, 0] = 1.0
+    y = fw.block_weight_grad(g.view(SF).to(dev), c.to(E4).to(dev), torch.ones(1, 1, device=dev).to(E8), out_dtype=out).cpu()
+    assert y[:12].isnan().all() and not y[12:].isnan().any()
+    if out == SF:
+        assert torch.equal(y[12:15, 0], g.view(SF)[0, 12:15])
+
+
+@pytest.mark.gpu
 def test_weight_grad_of_far_scales_and_axes(dev):
     """Scales over the whole of bf16's range; leading axes; no groups at all."""
     gen = rng(6)
