@@ -225,6 +225,9 @@ __device__ __forceinline__ Scale<MODE> scale_from(uint32_t word, int e8m0)
 // s + 1 are under way before its first row needs them.
 // Loads past an operand's rows or past K are out of their buffer's range and
 // give zeros.
+// 8192^3 in tiles of 256 x 256: 396 us, 2.78 PFLOP/s, where the card is at its
+// power limit (matrix pipes busy 67% at some 2 GHz); with binary32 scales 448, with
+// binary32 outputs (tiles of 128 x 128) 1116.
 
 constexpr int kFar = (int)0x80000000;  // an offset past every range
 
@@ -469,7 +472,7 @@ __global__ __launch_bounds__(WM * WN * 64, (TileShape<MODE, BM, BN, WM, WN, NB>:
 // Up to 16 R rows of a (or of a group of it): w is read once, from global
 // memory straight into fragments.  A workgroup takes 16 columns, its W waves
 // the stages of K in turn; their sums are joined in LDS, in the waves' order.
-// Any alignment and any K.
+// Any alignment and any K.  1 x 5760 x 1920: 5.2 us, a launch and one trip to memory.
 template <int AF, int WF, int MODE, int R, int W, bool WORDS>
 __global__ __launch_bounds__(W * 64) void block_rows(BlockMMParams p, int tn)
 {
