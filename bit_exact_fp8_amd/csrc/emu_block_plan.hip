@@ -15,20 +15,13 @@ extern template void launch_block_kernel<1, 1>(const BlockMMParams &, const Bloc
 
 namespace {
 
-// Rows of E matrices laid out anew, with the leading dimension `ldo`, a
-// multiple of 128, and zeros past K.  A workgroup takes `rows` of them, the
-// first from row0 on.
-template <bool WORDS>
-__global__ __launch_bounds__(256) void block_repack(const int8_t *in, int64_t ld, int64_t stride, int64_t per, int64_t total,
-                                                    int64_t K, int8_t *out, int64_t ldo, int64_t row0, int rows)
+__global__ __launch_bounds__(256) void block_repack(RepackRows a, RepackRows b, int64_t of_a, int64_t base)
 {
-    const int chunks = (int)(ldo / 16);
-    const int64_t first = row0 + (int64_t)blockIdx.x * rows;
-    for (int i = threadIdx.x; i < rows * chunks; i += 256) {
-        const int64_t row = first + i / chunks, k = i % chunks * 16;
-        if (row >= total) return;
-        *reinterpret_cast<i32x4 *>(out + row * ldo + k) = load16<WORDS>(in + row / per * stride + row % per * ld, k, K);
-    }
+    const int64_t group = base + blockIdx.x;
+    if (group < of_a)
+        repack_rows(a, group);
+    else
+        repack_rows(b, group - of_a);
 }
 
 // The sums of S splits and the epilogue, four outputs a thread.
@@ -173,18 +166,19 @@ void launch_slice(int a_dtype, int w_dtype, BlockMMParams p, bool a_aligned, boo
     BlockPlan k = plan.kernel;
     k.words = in_words(p);
     char *ws = static_cast<char *>(p.ws);
+    RepackRows a{}, w{};
     if (plan.repack_a) {
-        repack_codes(p.a, p.lda, 0, p.M, p.M, p.K, reinterpret_cast<int8_t *>(ws), plan.ld, stream);
-        p.a = reinterpret_cast<const int8_t *>(ws);
+        a = repack_job(p.a, p.lda, 0, p.M, p.M, p.K, reinterpret_cast<int8_t *>(ws), plan.ld);
+        p.a = a.out;
         p.lda = plan.ld;
     }
     if (plan.repack_w) {
-        int8_t *w = reinterpret_cast<int8_t *>(ws + plan.a_bytes);
-        repack_codes(p.w, p.ldw, p.w_stride, p.N, p.E * p.N, p.K, w, plan.ld, stream);
-        p.w = w;
+        w = repack_job(p.w, p.ldw, p.w_stride, p.N, p.E * p.N, p.K, reinterpret_cast<int8_t *>(ws + plan.a_bytes), plan.ld);
+        p.w = w.out;
         p.ldw = plan.ld;
         p.w_stride = p.N * plan.ld;
     }
+    launch_repack(a, w, stream);
     if (plan.repack_a && plan.repack_w) p.K = plan.ld;
     float *part = k.S > 1 ? reinterpret_cast<float *>(ws + plan.a_bytes + plan.w_bytes) : nullptr;
     const bool a5 = a_dtype == EMU_DT_E5M2, w5 = w_dtype == EMU_DT_E5M2;
@@ -196,19 +190,17 @@ void launch_slice(int a_dtype, int w_dtype, BlockMMParams p, bool a_aligned, boo
 
 }  // namespace
 
-void repack_codes(const int8_t *in, int64_t ld, int64_t stride, int64_t per, int64_t total, int64_t K, int8_t *out, int64_t ldo,
-                  hipStream_t stream)
+RepackRows repack_job(const int8_t *in, int64_t ld, int64_t stride, int64_t per, int64_t total, int64_t K, int8_t *out, int64_t ldo)
 {
-    const int rows = (int)ceil_div(512, ldo / 16);  // some two chunks a thread
-    constexpr int64_t most = int64_t(1) << 22;      // workgroups of a launch
-    for (int64_t r = 0; r < total; r += most * rows) {
-        const int64_t left = ceil_div(total - r, rows);
-        const dim3 grid((unsigned)(left < most ? left : most));
-        if (((reinterpret_cast<uintptr_t>(in) | ld | stride) & 3) == 0)
-            hipLaunchKernelGGL((block_repack<true>), grid, dim3(256), 0, stream, in, ld, stride, per, total, K, out, ldo, r, rows);
-        else
-            hipLaunchKernelGGL((block_repack<false>), grid, dim3(256), 0, stream, in, ld, stride, per, total, K, out, ldo, r, rows);
-    }
+    const bool words = ((reinterpret_cast<uintptr_t>(in) | ld | stride) & 3) == 0;
+    return {in, ld, stride, per, total, K, out, ldo, (int)ceil_div(512, ldo / 16), words};  // (some two chunks a thread)
+}
+void launch_repack(const RepackRows &a, const RepackRows &b, hipStream_t stream)
+{
+    constexpr int64_t most = int64_t(1) << 22;  // workgroups of a launch
+    const int64_t of_a = repack_groups(a), all = of_a + repack_groups(b);
+    for (int64_t base = 0; base < all; base += most)
+        hipLaunchKernelGGL(block_repack, dim3((unsigned)(all - base < most ? all - base : most)), dim3(256), 0, stream, a, b, of_a, base);
 }
 
 int64_t block_mm_workspace(int64_t M, int64_t N, int64_t K, int E, bool grouped, bool fp32_out, bool a_aligned, bool w_aligned)

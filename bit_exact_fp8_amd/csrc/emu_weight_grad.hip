@@ -30,10 +30,15 @@ typedef short s16x8 __attribute__((ext_vector_type(8)));
 // what that left: each cut is exact, and no part is larger than the value.  Two
 // parts of an fp32 value are its nearest one (or cut, where that were an infinity)
 // and the nearest of what that left.
+// Workgroups from `groups` on lay out rows of codes.
 template <typename G, int PLANES>
 __global__ __launch_bounds__(256) void split_planes(const G *g, int64_t ldg, int64_t T, int64_t N, uint16_t *out, int64_t ldo,
-                                                    int64_t plane)
+                                                    int64_t plane, unsigned groups, RepackRows codes)
 {
+    if (blockIdx.x >= groups) {
+        repack_rows(codes, blockIdx.x - groups);
+        return;
+    }
     const uint32_t chunks = (uint32_t)(ldo / 8), id = blockIdx.x * 256 + threadIdx.x, row = id / chunks;
     const int64_t t = row;
     const int c = (int)(id - row * chunks) * 8, n = (int)N;
@@ -419,15 +424,22 @@ void launch_tiles(const WeightGradParams &p, const GradPlan &plan, float *part, 
         hipLaunchKernelGGL((grad_tiles<CF, PLANES, 128, 128, 2, 2, 2>), grid, dim3(256), 0, stream, p, (int)tn, (int)tk, plan.S, part);
 }
 
+// With the codes' rows in the first launch, where it has room for them.
 template <typename G, int PLANES>
-void launch_split(const WeightGradParams &p, uint16_t *out, int64_t ldo, hipStream_t stream)
+void launch_split(const WeightGradParams &p, uint16_t *out, int64_t ldo, RepackRows codes, hipStream_t stream)
 {
     int64_t step = (int64_t(1) << 30) / (ldo / 8);  // a launch's rows
     step = step < 1 ? 1 : step;
+    if (repack_groups(codes) > int64_t(1) << 22) {
+        launch_repack(codes, RepackRows{}, stream);
+        codes = RepackRows{};
+    }
     for (int64_t t = 0; t < p.T; t += step) {
         const int64_t rows = p.T - t < step ? p.T - t : step;
-        hipLaunchKernelGGL((split_planes<G, PLANES>), dim3((unsigned)ceil_div(rows * (ldo / 8), 256)), dim3(256), 0, stream,
-                           reinterpret_cast<const G *>(p.g) + t * p.ldg, p.ldg, rows, p.N, out + t * ldo, ldo, p.T * ldo);
+        const unsigned groups = (unsigned)ceil_div(rows * (ldo / 8), 256);
+        hipLaunchKernelGGL((split_planes<G, PLANES>), dim3(groups + (unsigned)repack_groups(codes)), dim3(256), 0, stream,
+                           reinterpret_cast<const G *>(p.g) + t * p.ldg, p.ldg, rows, p.N, out + t * ldo, ldo, p.T * ldo, groups, codes);
+        codes = RepackRows{};
     }
 }
 
@@ -451,28 +463,29 @@ hipError_t launch_weight_grad(int g_dtype, int c_dtype, const WeightGradParams &
     const GradPlan plan = make_plan(p.T, p.E, p.N, p.K, g_dtype, p.out_dtype != EMU_DT_FP32, g_aligned, c_aligned);
     char *at = static_cast<char *>(ws);
     p.planes = plan.planes;
+    RepackRows codes{};
+    if (plan.repack_c && p.T > 0) {
+        codes = repack_job(p.codes, p.ldc, 0, p.T, p.T, p.K, reinterpret_cast<int8_t *>(at + plan.g_bytes), plan.ldc);
+        p.codes = codes.out;
+        p.ldc = plan.ldc;
+    }
     if (plan.split_g && p.T > 0) {
         uint16_t *g = reinterpret_cast<uint16_t *>(at);
         if (g_dtype == EMU_DT_BF16)
-            launch_split<__bf16, 1>(p, g, plan.ldg, stream);
+            launch_split<__bf16, 1>(p, g, plan.ldg, codes, stream);
         else if (g_dtype == EMU_DT_FP16)
-            launch_split<_Float16, 2>(p, g, plan.ldg, stream);
+            launch_split<_Float16, 2>(p, g, plan.ldg, codes, stream);
         else if (plan.planes == 2)
-            launch_split<float, 2>(p, g, plan.ldg, stream);
+            launch_split<float, 2>(p, g, plan.ldg, codes, stream);
         else
-            launch_split<float, 3>(p, g, plan.ldg, stream);
+            launch_split<float, 3>(p, g, plan.ldg, codes, stream);
         p.g = g;
         p.ldg = plan.ldg;
         p.plane_stride = p.T * plan.ldg;
+    } else {
+        launch_repack(codes, RepackRows{}, stream);
     }
-    at += plan.g_bytes;
-    if (plan.repack_c && p.T > 0) {
-        int8_t *c = reinterpret_cast<int8_t *>(at);
-        repack_codes(p.codes, p.ldc, 0, p.T, p.T, p.K, c, plan.ldc, stream);
-        p.codes = c;
-        p.ldc = plan.ldc;
-    }
-    at += plan.c_bytes;
+    at += plan.g_bytes + plan.c_bytes;
     float *part = plan.S > 1 ? reinterpret_cast<float *>(at) : nullptr;
     const bool e4 = c_dtype == EMU_DT_E4M3FN, planes = plan.planes > 1;
     (e4 ? planes ? launch_tiles<0, true> : launch_tiles<0, false> : planes ? launch_tiles<1, true> : launch_tiles<1, false>)(

@@ -139,6 +139,33 @@ __device__ __forceinline__ i32x4 load16(const int8_t *row, int64_t k, int64_t K)
     return over < 16 ? __builtin_bit_cast(i32x4, bits >> (8 * (int)over)) : i32x4{0, 0, 0, 0};
 }
 
+// Rows of matrices of `per` rows each, `total` in all, laid out anew: 16-byte
+// aligned, with the leading dimension `ldo`, a multiple of 128, and zeros past K.
+// A workgroup takes `rows` of them.
+struct RepackRows {
+    const int8_t *in;
+    int64_t ld, stride, per, total, K;
+    int8_t *out;
+    int64_t ldo;
+    int rows;
+    bool words;  // the rows are aligned to 4 bytes
+};
+inline int64_t repack_groups(const RepackRows &j) { return j.total ? ceil_div(j.total, j.rows) : 0; }
+__device__ __forceinline__ void repack_rows(const RepackRows &j, int64_t group)
+{
+    const int chunks = (int)(j.ldo / 16);
+    const int64_t first = group * j.rows, matrix = j.per < j.total ? first / j.per : 0, at = first - matrix * j.per;
+    const int64_t left = j.total - first;
+    const int rows = left < j.rows ? (int)left : j.rows;
+    for (int i = threadIdx.x; i < rows * chunks; i += 256) {
+        const int r = i / chunks, k = (i - r * chunks) * 16;
+        int64_t m = matrix, row = at + r;
+        while (row >= j.per) row -= j.per, ++m;
+        const int8_t *from = j.in + m * j.stride + row * j.ld;
+        *reinterpret_cast<i32x4 *>(j.out + (first + r) * j.ldo + k) = j.words ? load16<true>(from, k, j.K) : load16<false>(from, k, j.K);
+    }
+}
+
 // A wave's outputs: fragment (i, j) holds the outputs of row m + 16 i from
 // column n + 16 j + 4 (lane / 16) on, four to a lane; `whole`: all of them lie
 // within the matrix; `add`: a bias for each column.  Outputs of 16 bits go out eight to a lane: the quarters of
