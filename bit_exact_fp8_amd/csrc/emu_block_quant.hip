@@ -20,7 +20,7 @@ constexpr float kLargest = Q == EMU_DT_E4M3FN ? 448.0f : 57344.0f;
 // A block's scale and what makes codes of it.
 struct BlockScale {
     float value;      // the scale
-    float hi, lo;     // its reciprocal: exact in hi (e8m0), or the sum of both to within 2^-44
+    float by;         // its reciprocal: exact (e8m0), or within 2^-23
     uint32_t byte;    // e8m0
 };
 
@@ -39,13 +39,11 @@ __device__ __forceinline__ BlockScale scale_of(float most)
         const uint32_t b = (uint32_t)(e < 1 ? 1 : e);
         s.byte = finite ? b : 255;
         s.value = finite ? __uint_as_float(b << 23) : NAN;
-        s.hi = finite ? __uint_as_float((254u - b) << 23) : NAN;
-        s.lo = 0.0f;
+        s.by = finite ? __uint_as_float((254u - b) << 23) : NAN;
     } else {
         const float v = most / kLargest<Q>;
         s.value = finite ? (v > kLeastScale ? v : kLeastScale) : NAN;
-        s.hi = __builtin_amdgcn_rcpf(s.value);
-        s.lo = __builtin_fmaf(-s.value, s.hi, 1.0f) * s.hi;
+        s.by = __builtin_amdgcn_rcpf(s.value);
         s.byte = 0;
     }
     return s;
@@ -63,45 +61,9 @@ __device__ __forceinline__ float quotient_to_odd(float x, float s)
     return plain ? __uint_as_float((bits - ((__float_as_uint(off) ^ bits) >> 31)) | 1) : y;
 }
 
-// 0 where y lies on a border between two codes: halfway between normal ones,
-// or (below 2^-6, 2^-14) at any of the places that hold subnormal ones' borders.
 template <int Q>
-__device__ __forceinline__ uint32_t from_border(float y)
+__device__ __forceinline__ uint2 nearest_codes(const f32x8 &y)
 {
-    constexpr uint32_t half = Q == EMU_DT_E4M3FN ? 0x80000 : 0x100000;
-    const uint32_t bits = __float_as_uint(y), size = bits & 0x7FFFFFFF;
-    const bool normal = size >= (Q == EMU_DT_E4M3FN ? 0x3C800000u : 0x38800000u);
-    return normal ? (bits & (2 * half - 1)) ^ half : size ? bits & (half - 1) : 1;
-}
-
-// 8 codes of v.  Binary32 scales: v times the reciprocal's two parts is the
-// quotient to within 2^-30 before it is rounded, so it may fall on a border
-// between two codes, but never past one; where any does, all are divided.
-// Values past the type's largest (by the scale's own rounding) become it.
-template <int Q, bool E8M0>
-__device__ __forceinline__ uint2 codes_of(const f32x8 &v, const BlockScale &s)
-{
-    f32x8 y;
-    if (E8M0) {
-        y = v * s.hi;
-    } else {
-        uint32_t least = ~0u;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            y[i] = __builtin_fmaf(v[i], s.hi, v[i] * s.lo);
-            const uint32_t last = from_border<Q>(y[i]);
-            least = last < least ? last : least;
-        }
-        if (__any(least == 0 || s.value < 7.888609052e-31f)) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = quotient_to_odd(v[i], s.value);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float m = kLargest<Q>;
-            y[i] = y[i] > m ? m : y[i] < -m ? -m : y[i];  // (a NaN stays)
-        }
-    }
     uint32_t r[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -114,6 +76,29 @@ __device__ __forceinline__ uint2 codes_of(const f32x8 &v, const BlockScale &s)
         }
     }
     return make_uint2(r[0], r[1]);
+}
+
+// 8 codes of v.  Binary32 scales: v times the reciprocal is the quotient to
+// within 2^-22, so that 2^-21 less and more enclose it, and where both have one
+// code it is the quotient's; else all are divided.  Values past the type's largest
+// (by the scale's own rounding) become it.
+template <int Q, bool E8M0>
+__device__ __forceinline__ uint2 codes_of(const f32x8 &v, const BlockScale &s)
+{
+    if (E8M0) return nearest_codes<Q>(v * s.by);
+    constexpr float most = kLargest<Q>;
+    f32x8 y;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = __builtin_amdgcn_fmed3f(v[i] * s.by, -most, most);
+    uint2 codes = nearest_codes<Q>(y * 0.99999952f);
+    const uint2 above = nearest_codes<Q>(y * 1.00000048f);
+    if (__any(codes.x != above.x || codes.y != above.y)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = __builtin_amdgcn_fmed3f(quotient_to_odd(v[i], s.value), -most, most);
+        codes = nearest_codes<Q>(y);
+    }
+    const bool nan = s.value != s.value;
+    return nan ? make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu) : codes;
 }
 
 template <typename T>
@@ -248,7 +233,7 @@ __global__ __launch_bounds__(256) void quant_rows(BlockQuantParams p, int per_ro
 // ---- blocks of 128 x 128 -------------------------------------------------
 
 // A workgroup of 256 has a block: 16 lanes a row, 8 rows a thread (8 matrices of
-// 4096 x 4096 fp32: 122 us, 5.5 TB/s).
+// 4096 x 4096 fp32: 118 us, 5.7 TB/s).
 template <typename X, int Q, bool E8M0>
 __global__ __launch_bounds__(256) void quant_squares(BlockQuantParams p)
 {
@@ -309,8 +294,8 @@ __device__ __forceinline__ f32x8 sigmoid(const f32x8 &a, f32x8 &e)
 }
 
 // KEEP: gate's and up's own codes are stored too.  Two blocks a lane: 1023 x 1925
-// with binary32 scales take 6.5 us (6.0 with one, when twice the waves hide the
-// instructions' latencies), but the gradient of 8192 x 8192 97 and 104.
+// with binary32 scales take 6.2 us (some 0.5 less with one, when twice the waves
+// hide the instructions' latencies), but the gradient of 8192 x 8192 97 and 104.
 template <typename X, int Q, bool E8M0, bool KEEP, int ITEMS>
 __global__ __launch_bounds__(256) void swiglu_rows(SwigluParams p, int per_row)
 {
