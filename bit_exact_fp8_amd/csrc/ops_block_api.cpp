@@ -53,9 +53,9 @@ const char *refused(const emu::BlockMMParams &p, int a_dtype, int w_dtype, int s
 const char *refused_pointers(const emu::BlockMMParams &p, int s_type, emu_dtype bias_dtype)
 {
     const int64_t blocks = blocks_of(p.K), wide = blocks_of(p.N);
-    if (!p.out || (p.K > 0 && p.E > 0 && (!p.a || !p.w || !p.sa || !p.sw))) return "null pointer";
+    if (!p.out || (p.K > 0 && (!p.a || !p.w || !p.sa || !p.sw))) return "null pointer";
     if (bad_ld(p.ldo, p.N, p.M)) return "leading dimension smaller than a row";
-    if (p.K > 0 && p.E > 0) {
+    if (p.K > 0) {
         if (bad_ld(p.lda, p.K, p.M) || bad_ld(p.ldw, p.K, p.N)) return "leading dimension smaller than a row";
         if (p.w_stride < 0 || p.sw_stride < 0 || far(p.w_stride, p.E) || far(p.sw_stride, p.E) || p.sa_row < 0 || p.sa_block < 0 ||
             p.sw_row < 0 || p.sw_block < 0 || far(p.sa_row, p.M) || far(p.sa_block, blocks) || far(p.sw_row, wide) ||
@@ -267,6 +267,7 @@ emu_status emu_grouped_block_scaled_mm(const void *a, emu_dtype a_dtype, int64_t
     if (T > kMaxGroupedRows || E > kMaxGroups) return unsupported("T above 2^24 or E above 65536");
     if (const char *text = too_large(p)) return unsupported(text);
     if (T == 0 || N == 0 || (E == 0 && !zero_rest)) return set_error(EMU_OK, "");
+    if (E == 0) p.K = 0;  // (no sum: zeros behind no group's rows, for which no operand is read or laid out)
     if (!ends && E > 0) return invalid("null pointer");
     if (!aligned_to(ends, ends_bits / 8)) return invalid("a pointer is not aligned to its element");
     if (const char *text = refused_pointers(p, s_type, EMU_DT_FP32)) return invalid(text);

@@ -1,0 +1,42 @@
+"""The block operators at their limits: calls without groups, and calls that one
+launch does not hold."""
+import pytest
+import torch
+
+import bit_exact_fp8_amd as fw
+from bit_exact_fp8_amd import block_operators
+from test_block_operators import E8, blocks, c_grouped, dev  # noqa: F401
+from test_operators import BF, E4, SF, note
+
+
+# ---- no group at all ---------------------------------------------------------
+@pytest.mark.parametrize("kw", [dict(K=250, lda=250, ldw=250), dict(a=17), dict(lda=257), dict(a=None), dict(lda=0), dict(od=2, K=250)])
+def test_no_groups_need_no_workspace(kw):
+    """With the size that the query gives such a call is not refused for it, whatever a's
+    rows look like, which are not read: the pointer's alignment is all that is left to refuse."""
+    lib = block_operators._lib()
+    assert lib.emu_grouped_block_scaled_mm_workspace(1000, 0, 300, kw.get("K", 256), kw.get("od", 0), 0, 0) == 0
+    assert c_grouped(E=0, ws=8, wsb=0, **kw) == 1
+    assert b"workspace is not 16-byte aligned" in lib.emu_last_error_message()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,K", [(1, 250), (65, 256), (100, 250), (900, 250), (900, 256)])
+@pytest.mark.parametrize("out", [BF, SF])
+def test_no_groups(dev, T, K, out):  # noqa: F811
+    note(f"grouped product {T}x300x{K} of no groups")
+    a = torch.zeros(T, K + 3, dtype=torch.uint8, device=dev)[:, 1:1 + K].view(E4)
+    args = (a, torch.empty(0, 300, K, dtype=E4, device=dev).transpose(1, 2), torch.zeros(T, blocks(K), device=dev).to(E8),
+            torch.empty(0, blocks(300), blocks(K), device=dev).to(E8).transpose(1, 2), torch.empty(0, dtype=torch.int32, device=dev))
+    y = fw.grouped_block_scaled_mm(*args, out_dtype=out)
+    assert y.shape == (T, 300) and not y.any()
+    given = torch.full((T, 300), 7.0, dtype=out, device=dev)
+    assert (fw.grouped_block_scaled_mm(*args, out_dtype=out, out=given) == 7).all()
+    # without operands, through the C ABI, and with more workspace than is asked for
+    given.fill_(7.0)
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device=dev)
+    torch.cuda.synchronize(dev)
+    status = c_grouped(a=None, w=None, sa=None, sw=None, ends=None, E=0, M=T, K=K, lda=K, ldw=K, od=2 if out == SF else 0, out=given.data_ptr(),
+                       ws=ws.data_ptr(), wsb=ws.numel())
+    torch.cuda.synchronize(dev)
+    assert status == 0 and not given.any()
