@@ -410,10 +410,11 @@ void with_types(int x_dtype, int q_dtype, bool e8m0, F f)
         with_q(std::false_type{});
 }
 
-// Rows of a launch: its blocks are counted in 31 bits.
+// Rows of a launch: 2^28 blocks, of 8 threads each where a lane has two, so that
+// its grid stays below 2^32 threads (and blocks are counted in 31 bits).
 int64_t rows_of_launch(int64_t T, int64_t per_row)
 {
-    const int64_t most = (int64_t(1) << 30) / per_row;
+    const int64_t most = (int64_t(1) << 28) / per_row;
     return T < most ? T : most < 1 ? 1 : most;
 }
 // Blocks of a group of 16 lanes.

@@ -40,3 +40,39 @@ def test_no_groups(dev, T, K, out):  # noqa: F811
                        ws=ws.data_ptr(), wsb=ws.numel())
     torch.cuda.synchronize(dev)
     assert status == 0 and not given.any()
+
+
+# ---- more than one launch holds -------------------------------------------------
+def alike(a, b):
+    return torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def repeated(t, T):
+    """`t` over and over, T rows."""
+    return t.repeat(-(-T // len(t)), 1)[:T]
+
+
+@pytest.mark.gpu
+def test_more_blocks_than_a_launch(dev):  # noqa: F811
+    """2^29 rows of one value, of which a grid of 2^32 threads would be one launch:
+    those of a small call over and over, at every border between launches too."""
+    T, period = 2 ** 29 + 33, 2 ** 20 + 7
+    gen = torch.Generator(device=dev).manual_seed(5)
+    gate, up, g = (torch.randn(period, 1, device=dev, generator=gen).to(BF) for _ in range(3))
+    want, want_h = fw.block_quant(gate), fw.swiglu_block_quant(gate, up, keep=True)
+    want_d = fw.swiglu_block_backward(g, want_h.kept, want_h.kept_scale)
+
+    def check(got, want):
+        for y, w in zip(got, want):
+            assert len(y) == T
+            for r in range(0, T, period):
+                assert alike(y[r:r + period], w[:min(period, T - r)]), r
+
+    note(f"block codes of {T} rows")
+    gate, up, g = (repeated(t, T) for t in (gate, up, g))
+    check(fw.block_quant(gate), want)
+    note(f"gated activation of {T} rows")
+    h = fw.swiglu_block_quant(gate, up, keep=True)
+    check(h, want_h)
+    note(f"gated activation's gradient of {T} rows")
+    check([fw.swiglu_block_backward(g, h.kept, h.kept_scale)], [want_d])
