@@ -140,7 +140,9 @@ int mode_of(bool fp32_out, bool e8m0) { return fp32_out ? kExact : e8m0 ? kHardw
 
 // A launch's rows (dense) and columns, so that its grid stays below 2^32
 // threads: of groups, whose rows one launch has to hold, fewer columns at a time.
+// Without K block_join alone makes the outputs, four a thread: at most 2^33 of them.
 constexpr int64_t kSliceM = 1 << 18, kSliceN = 1 << 17;
+int64_t slice_m(int64_t M, int64_t K, bool grouped) { return grouped ? M : K ? kSliceM : (int64_t(1) << 33) / kSliceN; }
 int64_t slice_n(int64_t M, int64_t K, int E, bool grouped)
 {
     if (!grouped) return kSliceN;
@@ -207,8 +209,8 @@ int64_t block_mm_workspace(int64_t M, int64_t N, int64_t K, int E, bool grouped,
 {
     if (K == 0) return 0;
     int64_t most = 0;
-    const int64_t step = slice_n(M, K, E, grouped), slice_m = grouped ? M : kSliceM;
-    for (int64_t m : {M < slice_m ? M : slice_m, M % slice_m})
+    const int64_t step = slice_n(M, K, E, grouped), high = slice_m(M, K, grouped);
+    for (int64_t m : {M < high ? M : high, M % high})
         for (int64_t n : {N < step ? N : step, N % step}) {
             if (!m || !n) continue;
             for (bool e8m0 : {false, true}) {
@@ -224,11 +226,11 @@ hipError_t launch_block_mm(int a_dtype, int w_dtype, const BlockMMParams &p, boo
 {
     const int64_t size = p.out_dtype == EMU_DT_FP32 ? 4 : 2, unit = p.e8m0 ? 1 : 4;
     const bool grouped = p.ends != nullptr;
-    const int64_t step = slice_n(p.M, p.K, p.E, grouped), slice_m = grouped ? p.M : kSliceM;
-    for (int64_t m = 0; m < p.M; m += slice_m)
+    const int64_t step = slice_n(p.M, p.K, p.E, grouped), high = slice_m(p.M, p.K, grouped);
+    for (int64_t m = 0; m < p.M; m += high)
         for (int64_t n = 0; n < p.N; n += step) {
             BlockMMParams q = p;
-            q.M = p.M - m < slice_m ? p.M - m : slice_m;
+            q.M = p.M - m < high ? p.M - m : high;
             q.N = p.N - n < step ? p.N - n : step;
             if (p.K) {
                 q.a = p.a + m * p.lda;

@@ -76,3 +76,16 @@ def test_more_blocks_than_a_launch(dev):  # noqa: F811
     check(h, want_h)
     note(f"gated activation's gradient of {T} rows")
     check([fw.swiglu_block_backward(g, h.kept, h.kept_scale)], [want_d])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N", [(2 ** 18, 2 ** 16 + 4), (2 ** 16 + 3, 2 ** 17 + 5)])
+def test_more_outputs_than_a_launch(dev, M, N):  # noqa: F811
+    """Without K the bias is every row, also where there are more than 2^34 outputs or slices of them."""
+    note(f"block product {M}x{N}x0")
+    b = torch.randn(N, device=dev, generator=torch.Generator(device=dev).manual_seed(7)).to(BF)
+    z = lambda *s: torch.empty(*s, dtype=E4, device=dev)  # noqa: E731
+    y = fw.block_scaled_mm(z(M, 0), z(N, 0).t(), torch.empty(M, 0, device=dev), torch.empty(blocks(N), 0, device=dev).t(), bias=b)
+    assert y.shape == (M, N)
+    for r in range(0, M, 4096):
+        assert (y[r:r + 4096] == b).all(), r
