@@ -5,8 +5,8 @@ import torch
 
 import bit_exact_fp8_amd as fw
 from bit_exact_fp8_amd import block_operators
-from test_block_operators import E8, blocks, c_grouped, dev  # noqa: F401
-from test_operators import BF, E4, SF, note
+from test_block_operators import E8, blocks, c_grouped, check_grouped, dev, exact_codes, spans, spread  # noqa: F401
+from test_operators import BF, E4, SF, f64, note, rng
 
 
 # ---- no group at all ---------------------------------------------------------
@@ -89,3 +89,38 @@ def test_more_outputs_than_a_launch(dev, M, N):  # noqa: F811
     assert y.shape == (M, N)
     for r in range(0, M, 4096):
         assert (y[r:r + 4096] == b).all(), r
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("given", [False, True])
+@pytest.mark.parametrize("ends,T,K,pad", [([1, 2], 3, 48, (0, 0)), ([0, 3], 3, 48, (3, 5)), ([2], 5, 33, (0, 0)), ([70, 290], 300, 48, (0, 0)),
+                                          ([130, 280], 300, 33, (0, 0)), ([200, 200], 300, 32, (0, 5))])
+def test_grouped_columns_of_several_launches(dev, ends, T, K, pad, given):  # noqa: F811
+    """More columns than a launch takes: of few rows, of tiles, and of operands laid out anew for each launch."""
+    check_grouped(dev, ends, T, 2 ** 17 + 130, K, exact=True, given=given, pad=pad)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("given", [False, True])
+@pytest.mark.parametrize("T,K", [(300, 16), (300, 33), (2000, 16)])
+def test_many_groups_of_several_launches(dev, T, K, given):  # noqa: F811
+    """As many groups as there may be, of which a launch takes a few hundred columns."""
+    E, N = 65536, 514
+    note(f"grouped product {T}x{N}x{K} of {E} groups given={given}")
+    a, sa, av = exact_codes(rng(T + K), T, K, 1, E4, E8)
+    gen = torch.Generator(device=dev).manual_seed(T)
+    w = torch.randint(-1, 2, (E, N, K), device=dev, generator=gen, dtype=torch.int8).to(BF).to(E4)
+    sw = torch.randint(127, 129, (E, blocks(N), blocks(K)), device=dev, generator=gen, dtype=torch.uint8).view(E8)
+    ends = torch.randint(0, T - 9, (E,), generator=rng(K)).sort().values
+    ends[-1] = T - 9
+    o = torch.full((T, N + 3), 7.0, dtype=BF, device=dev)[:, 2:2 + N] if given else None
+    y = fw.grouped_block_scaled_mm(a.to(dev), w.transpose(1, 2), sa.to(dev), sw.transpose(1, 2), ends.to(dev), out=o)
+    want = torch.full((T, N), 7.0 if given else 0.0, dtype=f64, device=dev)
+    av = av.to(dev)
+    for e, (first, end) in enumerate(spans(ends.tolist(), T)):
+        if end > first:
+            wv = w[e].to(f64) * spread(sw[e].float().to(f64), N, K, 128)
+            want[first:end] = av[first:end] @ wv.t().contiguous()
+    assert torch.equal(y, want.to(BF))
+    if given:
+        assert (o._base[:, :2] == 7).all() and (o._base[:, 2 + N:] == 7).all()
