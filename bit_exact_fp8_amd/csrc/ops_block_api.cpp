@@ -76,6 +76,14 @@ const char *too_large(const emu::BlockMMParams &p)
         return "scales' rows more than 2^20 apart";
     return nullptr;
 }
+// Whether E matrices of N rows of K overlap, which have to lie one after the
+// other or with their rows among each other: workgroups would write over each other.
+bool overlapping(int64_t ld, int64_t stride, int64_t E, int64_t N, int64_t K)
+{
+    if (E <= 1) return false;
+    if (N == 1 || stride >= ld) return stride < (N - 1) * ld + K;
+    return stride < K || ld < (E - 1) * stride + K;
+}
 const char *grad_too_large(int64_t T, int64_t E, int64_t N, int64_t K)
 {
     if (T > int64_t(1) << 30 || E > kMaxGroups) return "T above 2^30 or E above 65536";
@@ -299,6 +307,7 @@ emu_status emu_block_weight_grad(const void *g, emu_dtype g_dtype, int64_t ldg, 
     if (!out || (T > 0 && (!g || !codes || !scales))) return invalid("null pointer");
     if (bad_ld(ldo, K, N) || out_stride < 0 || (E > 1 && (out_stride < 1 || far(out_stride, E))))
         return invalid("leading dimension smaller than a row, or a bad stride");
+    if (overlapping(ldo, out_stride, E, N, K)) return invalid("the output's matrices overlap");
     if (T > 0 && (bad_ld(ldg, N, T) || bad_ld(ldc, K, T))) return invalid("leading dimension smaller than a row");
     if (T > 0 && (s_row < 0 || s_block < 0 || far(s_row, T) || far(s_block, blocks_of(K)))) return invalid("a negative stride, or one too large");
     const size_t size = size_of(g_dtype);

@@ -150,7 +150,8 @@ EMU_API size_t emu_grouped_block_scaled_mm_workspace(int64_t T, int64_t E, int64
  * added in binary32; an out of no rows is 0.
  * ends NULL: one sum over all rows, out [N, K].  Else E sums by groups of
  * rows, as in emu_grouped_block_scaled_mm: out [E, N, K], out_stride elements
- * between matrices, and rows behind the last group's take no part.
+ * between matrices, which lie one after the other or row by row beside each
+ * other, and rows behind the last group's take no part.
  * workspace: emu_block_weight_grad_workspace(...) bytes, 16-byte aligned (E =
  * 0: no groups); `aligned` says that the pointer and the rows' distance in
  * bytes are multiples of 16 and the leading dimension is at most

@@ -5,7 +5,7 @@ import torch
 
 import bit_exact_fp8_amd as fw
 from bit_exact_fp8_amd import block_operators
-from test_block_operators import E8, blocks, c_grouped, check_grouped, dev, exact_codes, spans, spread  # noqa: F401
+from test_block_operators import E8, blocks, c_grouped, c_weight_grad, check_grouped, dev, exact_codes, spans, spread  # noqa: F401
 from test_operators import BF, E4, SF, f64, note, rng
 
 
@@ -124,3 +124,30 @@ def test_many_groups_of_several_launches(dev, T, K, given):  # noqa: F811
     assert torch.equal(y, want.to(BF))
     if given:
         assert (o._base[:, :2] == 7).all() and (o._base[:, 2 + N:] == 7).all()
+
+
+# ---- outputs that meet themselves ------------------------------------------------
+@pytest.mark.parametrize("kw,fine", [(dict(os=64 * 256), True), (dict(os=64 * 256 - 1), False), (dict(os=1), False), (dict(os=255), False),
+                                     (dict(os=300, ldo=900), True), (dict(os=256, ldo=768), True), (dict(os=256, ldo=767), False),
+                                     (dict(os=300, ldo=855), False), (dict(os=63 * 300 + 256, ldo=300), True),
+                                     (dict(os=63 * 300 + 255, ldo=300), False), (dict(N=1, os=256, ldo=256), True),
+                                     (dict(N=1, os=255, ldo=256), False)])
+def test_weight_grad_outputs_apart(kw, fine):
+    """Matrices one after the other or row by row among each other, but not over each other
+    (all that is left to refuse then is the workspace's alignment)."""
+    assert c_weight_grad(ends=16, E=3, ws=8, **kw) == 1
+    text = block_operators._lib().emu_last_error_message()
+    assert (b"workspace is not 16-byte aligned" in text) == fine and (b"overlap" in text) != fine
+
+
+@pytest.mark.gpu
+def test_weight_grad_of_interleaved_outputs(dev):  # noqa: F811
+    """Experts' matrices row by row beside each other, as [N, E, K] holds them; over each other they are refused."""
+    T, N, K, ends = 90, 40, 130, torch.tensor([20, 50, 90], device=dev)
+    c, s, _ = exact_codes(rng(1), T, K, 1, E4, E8)
+    g = torch.randint(-2, 3, (T, N), generator=rng(2)).to(BF).to(dev)
+    out = torch.empty(N, 3, K, dtype=BF, device=dev).transpose(0, 1)
+    want = fw.block_weight_grad(g, c.to(dev), s.to(dev), ends)
+    assert torch.equal(fw.block_weight_grad(g, c.to(dev), s.to(dev), ends, out=out), want)
+    with pytest.raises(fw.EmuError):
+        fw.block_weight_grad(g, c.to(dev), s.to(dev), ends, out=out._base.as_strided((3, N, K), (N * K - 1, K, 1)))
