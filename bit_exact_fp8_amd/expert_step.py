@@ -42,6 +42,17 @@ def _product(codes, scale, weight, weight_scale, ends, out_dtype):
                                        out_dtype=out_dtype)
 
 
+def _joined(rows, order, T, c):
+    """[T, n]: of rows by expert each token's c, added in the order of its choices."""
+    at = torch.empty_like(order)
+    at[order] = torch.arange(T * c, device=order.device)
+    rows = rows[at].view(T, c, rows.shape[1])
+    out = rows[:, 0]
+    for j in range(1, c):
+        out = out + rows[:, j]
+    return out
+
+
 class Kept(NamedTuple):
     """What the forward pass leaves for the gradient."""
     order: torch.Tensor        # the rows' places among (token, choice), by expert
@@ -68,8 +79,7 @@ def forward(x: torch.Tensor, up: Projection, down: Projection, choice: torch.Ten
     F = both.shape[1] // 2
     h = ops.swiglu_block_quant(both[:, :F], both[:, F:], keep=True)
     y = _product(h.codes, h.scale, down.codes, down.scale, ends, torch.float32)
-    out = torch.zeros(T, x.shape[1], device=x.device)
-    out.index_add_(0, order // c, y * share.reshape(-1)[order, None])
+    out = _joined(y * share.reshape(-1)[order, None], order, T, c)
     return out.to(x.dtype), Kept(order, ends, codes, scale, h)
 
 
@@ -92,8 +102,7 @@ def backward(grad: torch.Tensor, kept: Kept, up: Projection, down: Projection, s
     grad_up = ops.block_weight_grad(grad_both, kept.x, kept.x_scale, kept.ends, out_dtype=torch.float32)
     codes, scale = ops.block_quant(grad_both)
     grad_rows = _product(codes, scale, up.turned, up.turned_scale, kept.ends, torch.float32)
-    grad_x = torch.zeros(T, grad.shape[1], device=grad.device).index_add_(0, kept.order // c, grad_rows)
-    return Gradients(grad_x.to(grad.dtype), grad_up, grad_down)
+    return Gradients(_joined(grad_rows, kept.order, T, c).to(grad.dtype), grad_up, grad_down)
 
 
 def main(argv=None):

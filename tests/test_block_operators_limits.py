@@ -6,7 +6,7 @@ import torch
 import bit_exact_fp8_amd as fw
 from bit_exact_fp8_amd import block_operators
 from test_block_operators import E8, blocks, c_grouped, c_weight_grad, check_grouped, dev, exact_codes, spans, spread  # noqa: F401
-from test_operators import BF, E4, SF, f64, note, rng
+from test_operators import BF, E4, SF, f64, note, rand, rng
 
 
 # ---- no group at all ---------------------------------------------------------
@@ -151,3 +151,37 @@ def test_weight_grad_of_interleaved_outputs(dev):  # noqa: F811
     assert torch.equal(fw.block_weight_grad(g, c.to(dev), s.to(dev), ends, out=out), want)
     with pytest.raises(fw.EmuError):
         fw.block_weight_grad(g, c.to(dev), s.to(dev), ends, out=out._base.as_strided((3, N, K), (N * K - 1, K, 1)))
+
+
+# ---- sums over a token's choices --------------------------------------------------
+@pytest.mark.gpu
+def test_expert_step_adds_choices_in_their_order(dev):  # noqa: F811
+    """A token's experts' outputs, and its inputs' gradients, are added in the order
+    of its choices: the same bits on every run."""
+    from bit_exact_fp8_amd import expert_step as es
+    T, n, hidden, E, c = 700, 256, 128, 12, 5
+    gen = rng(4)
+    x, grad, share = rand(gen, T, n).to(dev), rand(gen, T, n).to(dev), torch.rand(T, c, generator=gen).to(dev)
+    up, down = es.project(rand(gen, E, 2 * hidden, n, std=n ** -0.5).to(dev)), es.project(rand(gen, E, n, hidden, std=0.1).to(dev))
+    choice = torch.randint(0, E, (T, c), generator=gen).to(dev)  # (the same expert twice too)
+    with torch.no_grad():
+        out, kept = es.forward(x, up, down, choice, share)
+        g = es.backward(grad, kept, up, down, share)
+
+        def joined(rows):
+            """Of rows by expert: each token's, added one after the other."""
+            at = torch.empty_like(kept.order)
+            at[kept.order] = torch.arange(T * c, device=dev)
+            rows = rows[at].view(T, c, n)
+            y = rows[:, 0]
+            for j in range(1, c):
+                y = y + rows[:, j]
+            return y
+
+        y = es._product(kept.h.codes, kept.h.scale, down.codes, down.scale, kept.ends, SF)
+        assert torch.equal(out, joined(y * share.reshape(-1)[kept.order, None]))
+        rows = grad[kept.order // c] * share.reshape(-1)[kept.order, None]
+        codes, scale = fw.block_quant(rows)
+        grad_h = es._product(codes, scale, down.turned, down.turned_scale, kept.ends, SF)
+        codes, scale = fw.block_quant(fw.swiglu_block_backward(grad_h, kept.h.kept, kept.h.kept_scale))
+        assert torch.equal(g.x, joined(es._product(codes, scale, up.turned, up.turned_scale, kept.ends, SF)))
