@@ -113,8 +113,9 @@ def block_scaled_mm(mat1: torch.Tensor, mat2: torch.Tensor, scale_a: torch.Tenso
     mat1 [M, K] row-major with scale_a [M, blocks of K], as ``block_quant``
     gives them; mat2 [K, N] column-major with scale_b [blocks of K, blocks of N]
     (``w.t()`` and ``scale.t()`` of a row-major ``w [N, K]`` in blocks of
-    128 x 128).  Codes of either type, scales of one type and of any strides,
-    any sizes and alignments.  bias [N] of out_dtype or float32.
+    128 x 128).  Codes of either type, scales of one type and of any strides
+    (rows of them at most 2^20 apart), any sizes (K up to 2^22) and alignments.
+    bias [N] of out_dtype or float32.
 
     Blocks' sums are added in float32.  Within a block, outputs of 16 bits are
     made by the matrix instruction of these codes, which adds each 8 products
@@ -131,8 +132,9 @@ def grouped_block_scaled_mm(mat1: torch.Tensor, mat2: torch.Tensor, scale_a: tor
     mat2 [E, K, N] with scale_b [E, blocks of K, blocks of N] (``w.transpose(1,
     2)`` and the like of ``w [E, N, K]``); ends [E] int32 or int64, on the
     device and read there alone: an end below the one before counts as that one,
-    one past the rows as the last row's.  Groups may be empty.  Rows behind the
-    last group's are 0, and in an ``out`` that is given left as they are."""
+    one past the rows as the last row's.  Groups may be empty, and there may be
+    none.  Rows behind the last group's are 0, and in an ``out`` that is given
+    left as they are."""
     return (_OPS or _binding()).grouped_block_scaled_mm(mat1, mat2, scale_a, scale_b, ends, out_dtype, out)
 
 
@@ -145,7 +147,8 @@ def block_weight_grad(grad: torch.Tensor, codes: torch.Tensor, scale: torch.Tens
     two, under which bf16 holds x exactly).  ends [E]: a sum for each group of
     rows, [E, N, K], as in ``grouped_block_scaled_mm``; rows behind the last
     group's take no part, and an empty group's sum is 0.  Products are exact (of
-    a float32 grad within 2^-17 where out_dtype has 16 bits) and added in
-    float32; out_dtype is grad's where none is given.  grad in float16 or float32
-    takes two or three times as long as in bfloat16."""
+    a float32 grad within 2^-17 where out_dtype has 16 bits; what of it lies below
+    2^-133 counts as 0) and added in float32; out_dtype is grad's where none is
+    given.  The matrices of an ``out`` that is given must not overlap.  grad in
+    float16 or float32 takes two to four times as long as in bfloat16."""
     return (_OPS or _binding()).block_weight_grad(grad, codes, scale, ends, out_dtype, out)

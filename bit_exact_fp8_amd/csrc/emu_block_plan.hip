@@ -94,6 +94,10 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int E, bool grouped, int mode, b
     const bool ra = needs_repack(K, a_aligned), rw = needs_repack(K, w_aligned);
     // Operands that are not aligned are laid out anew for tiles, which for up to
     // 64 rows (of each group, in the mean) takes longer than to read them in words.
+    // More waves for a longer K: 1 x 4096 x 4099 takes 6.7 us with 16 of them and 8.2
+    // with 4, 32 x 4096 x 4099 11.7 with 8 and 12.8 with 4; up to K = 4096 they are
+    // within 0.6 us (1921: 5.2 and 5.8, 8.9 and 9.0).  64 rows, K = 4099: 17.8 with 8,
+    // 20.8 with 4, 28.5 with 16.
     const int64_t mean = mean_rows(M, E, grouped);
     if ((mean <= 64 && (ra || rw)) || K == 0) {
         k.rows = mean <= 16 || K == 0 ? 1 : mean <= 32 ? 2 : 4;
@@ -123,7 +127,9 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int E, bool grouped, int mode, b
     // Up to 16 rows read w once, straight into registers, and wait for nothing,
     // but read a again for every 16 columns (16 x 4096 x 4096: 10.0 us, in tiles
     // 11.2; 16 x 8192 x 8192: 24.2 and 16.7).  Groups take tiles in any case: 32 x
-    // 4096 x 2048 over 16 of them 29.9 us, in tiles 24.2.
+    // 4096 x 2048 over 16 of them 29.9 us, in tiles 24.2.  With 4 waves 1 x 5760 x
+    // 1920 takes 4.9 us, with 16 6.0; x 8192 11.9 and 12.8, which on 4096 columns
+    // (x 8195, in words) is 12.4 and 9.8.
     if (!grouped && M <= 16 && 2.5 + (double)N * (double)K * (1.0 + (double)M / 16.0) / 7.5e6 < best) {
         k.tile = -1;
         k.S = k.rows = 1;

@@ -203,8 +203,10 @@ __device__ __forceinline__ Place place_of(int item, int64_t items, int per_row, 
 
 // ---- blocks of 1 x 128 ---------------------------------------------------
 
-// 16 lanes a block, two blocks a lane (2047 x 1920 bf16: 4.3 us, mostly the launch;
-// 14001 x 8057, past the cache, at the memory's rate).
+// 16 lanes a block, two blocks a lane, whose loads are under way together: bf16
+// with e8m0 scales take 3.8 us at 2047 x 1920, 16 at 4096 x 8192 and 62 at 16384 x
+// 8192, with one block 4.2, 19 and 78 (64 x 4096: 2.7 and 2.5).  14001 x 8057, past
+// the cache, runs at the memory's rate.
 template <typename X, int Q, bool E8M0, int ITEMS>
 __global__ __launch_bounds__(256) void quant_rows(BlockQuantParams p, int per_row)
 {
@@ -233,7 +235,7 @@ __global__ __launch_bounds__(256) void quant_rows(BlockQuantParams p, int per_ro
 // ---- blocks of 128 x 128 -------------------------------------------------
 
 // A workgroup of 256 has a block: 16 lanes a row, 8 rows a thread (8 matrices of
-// 4096 x 4096 fp32: 118 us, 5.7 TB/s).
+// 4096 x 4096 fp32: 112 us, 6.0 TB/s; 115 to 121 one call after the other).
 template <typename X, int Q, bool E8M0>
 __global__ __launch_bounds__(256) void quant_squares(BlockQuantParams p)
 {
@@ -293,9 +295,11 @@ __device__ __forceinline__ f32x8 sigmoid(const f32x8 &a, f32x8 &e)
     return p;
 }
 
-// KEEP: gate's and up's own codes are stored too.  Two blocks a lane: 1023 x 1925
-// with binary32 scales take 6.2 us (some 0.5 less with one, when twice the waves
-// hide the instructions' latencies), but the gradient of 8192 x 8192 97 and 104.
+// KEEP: gate's and up's own codes are stored too.  Two blocks a lane: 8192 x 8192
+// bf16 with e8m0 scales takes 65 us, with all three codes 87 (with one block 80 and
+// 97).  For few rows, where twice the waves hide the instructions' latencies, one
+// would take less: 5.4 us for 6.0 at 1023 x 1925 with binary32 scales, 3.0 for 3.6
+// at 64 x 4096; at 2240 x 10163 fp16 with all three it makes no difference (50).
 template <typename X, int Q, bool E8M0, bool KEEP, int ITEMS>
 __global__ __launch_bounds__(256) void swiglu_rows(SwigluParams p, int per_row)
 {
@@ -339,7 +343,9 @@ __global__ __launch_bounds__(256) void swiglu_rows(SwigluParams p, int per_row)
     }
 }
 
-// (8192 x 8192 bf16: 90 us, 6.0 TB/s)
+// (8192 x 8192 bf16: 89 us, 6.0 TB/s; one call after the other 81 in the first
+// 2 ms and 92 to 101 in the next 8.  With one block a lane as much; 1023 x 1925
+// 7.8 us, with one 5.9)
 template <typename G, int Q, bool E8M0, int ITEMS>
 __global__ __launch_bounds__(256) void swiglu_grad_rows(SwigluGradParams p, int per_row)
 {

@@ -388,7 +388,9 @@ GradPlan make_plan(int64_t T, int E, int64_t N, int64_t K, int g_dtype, bool out
     // The fastest estimate, as for the products: a round of 256 large tiles, or of
     // 512 small ones, two to a CU, or a rest of up to 256, one to a CU, as measured
     // (4096 x 4096 of 1024 rows: 43 us large, 51 small; 2048 x 2048: 35 and 20); a
-    // split of rows 5 us more and its sums at 4 TB/s, there and back.
+    // split of rows 5 us more and its sums at 4 TB/s, there and back.  (Stages of
+    // later planes, whose codes are looked at for infinities, are priced like those
+    // of one plane: 4096^3 takes 110 us in bf16, of fp32 g in two planes 257.)
     const int64_t stages = ceil_div(ceil_div(T, groups), kRows) * p.planes;
     double best = 0.0;
     p.S = 1;

@@ -123,7 +123,8 @@ EMU_API size_t emu_block_scaled_mm_workspace(int64_t M, int64_t N, int64_t K, em
  * (ends_bits 32 or 64), and read by the kernels alone: an end below the one
  * before counts as that one, one above T as T.  A group may have no rows.
  * Rows behind the last group's are left as they are, or become 0 where
- * zero_rest is not 0.  T up to 2^24, E up to 65536.
+ * zero_rest is not 0; without groups those are all rows, and no operand is
+ * read.  T up to 2^24, E up to 65536.
  */
 EMU_API emu_status emu_grouped_block_scaled_mm(const void *a, emu_dtype a_dtype, int64_t lda,
                                                const void *w, emu_dtype w_dtype, int64_t ldw, int64_t w_stride,
@@ -146,8 +147,9 @@ EMU_API size_t emu_grouped_block_scaled_mm_workspace(int64_t T, int64_t E, int64
  * g [T, N] bf16, fp16 or fp32; codes [T, K] e4m3fn or e5m2, blocks of 1 x 128
  * with e8m0 scales, that of row t and block b at t s_row + b s_block; out of
  * any of g's types.  Products are exact (those of fp16 and fp32 g as two and
- * three parts; for outputs of 16 bits those of fp32 g as two, within 2^-17) and
- * added in binary32; an out of no rows is 0.
+ * three parts; for outputs of 16 bits those of fp32 g as two, within 2^-17; what
+ * of g lies below 2^-133 counts as 0) and added in binary32; an out of no rows
+ * is 0.
  * ends NULL: one sum over all rows, out [N, K].  Else E sums by groups of
  * rows, as in emu_grouped_block_scaled_mm: out [E, N, K], out_stride elements
  * between matrices, which lie one after the other or row by row beside each
