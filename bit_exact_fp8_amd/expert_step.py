@@ -47,7 +47,7 @@ def _joined(rows, order, T, c):
     at = torch.empty_like(order)
     at[order] = torch.arange(T * c, device=order.device)
     rows = rows[at].view(T, c, rows.shape[1])
-    out = rows[:, 0]
+    out = rows[:, 0] if c else rows.new_zeros(T, rows.shape[2])
     for j in range(1, c):
         out = out + rows[:, j]
     return out

@@ -185,3 +185,15 @@ def test_expert_step_adds_choices_in_their_order(dev):  # noqa: F811
         grad_h = es._product(codes, scale, down.turned, down.turned_scale, kept.ends, SF)
         codes, scale = fw.block_quant(fw.swiglu_block_backward(grad_h, kept.h.kept, kept.h.kept_scale))
         assert torch.equal(g.x, joined(es._product(codes, scale, up.turned, up.turned_scale, kept.ends, SF)))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,c", [(5, 0), (0, 2)])
+def test_expert_step_without_rows(dev, T, c):  # noqa: F811
+    """Tokens of no expert, and no tokens: zeros, and no gradient."""
+    from bit_exact_fp8_amd import expert_step as es
+    up, down = es.project(rand(rng(1), 3, 256, 128).to(dev)), es.project(rand(rng(2), 3, 128, 128).to(dev))
+    x, choice, share = torch.ones(T, 128, device=dev), torch.zeros(T, c, dtype=torch.int64, device=dev), torch.zeros(T, c, device=dev)
+    out, kept = es.forward(x, up, down, choice, share)
+    g = es.backward(x, kept, up, down, share)
+    assert out.shape == g.x.shape == (T, 128) and not out.any() and not g.x.any() and not g.up.any() and not g.down.any()
